@@ -268,6 +268,56 @@ nvfp4_status nvfp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx,
                           void* y, int y_dtype, int64_t ldy, void* workspace,
                           size_t workspace_bytes, nvfp4_stream_t stream);
 
+/* Activations of the GEMM epilogue, evaluated in FP32:
+ *   RELU max(z, 0);  SILU z / (1 + e^-z);  GELU z/2 erfc(-z / sqrt 2);
+ *   GELU_TANH z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+typedef enum {
+  NVFP4_ACT_NONE = 0,
+  NVFP4_ACT_RELU = 1,
+  NVFP4_ACT_SILU = 2,
+  NVFP4_ACT_GELU = 3,
+  NVFP4_ACT_GELU_TANH = 4
+} nvfp4_activation;
+
+/*
+ * nvfp4_gemm_epilogue, nvfp4_linear_epilogue — nvfp4_gemm and nvfp4_linear with
+ * the rest of a projection layer in the GEMM's epilogue (the pages only name
+ * the 4-bit product, news §02; bias, activation and the residual stream are
+ * the model's own):
+ *   Y[i][j] = act(P[i][j] + bias[j]) + residual[i][j],
+ * P the FP32 product nvfp4_gemm would round; everything after it is FP32 and
+ * is rounded once to Y's type. With bias NULL, activation NONE and residual
+ * NULL these are nvfp4_gemm and nvfp4_linear, bit for bit.
+ *   bias        device bf16 [n] or NULL; 16-byte aligned; not inside Y.
+ *   activation  one of nvfp4_activation.
+ *   residual    device bf16 [m][ldr] or NULL; 16-byte aligned, ldr >= n,
+ *               ldr % 8 == 0 (ignored without a residual). It may be Y itself
+ *               (y_dtype bf16, ldr == ldy): the residual stream is then updated
+ *               in place. It may also be other columns of the matrix that Y is
+ *               a part of; any other overlap with Y is refused.
+ *   All other arguments, workspaces and launch rules as nvfp4_gemm and
+ *   nvfp4_linear. The bias and the residual may be written by work that
+ *   precedes the call in the stream.
+ * Errors: as nvfp4_gemm / nvfp4_linear; INVALID_ARG for an unknown activation,
+ * ldr < n or a refused overlap; MISALIGNED for the bias or the residual.
+ */
+nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a_codes, const uint8_t* a_sf,
+                                 const float* a_global, const uint8_t* b_codes,
+                                 const uint8_t* b_sf, const float* b_global,
+                                 const void* bias, nvfp4_activation activation,
+                                 const void* residual, int64_t ldr, void* y,
+                                 int y_dtype, int64_t ldy, int64_t m, int64_t n,
+                                 int64_t k, void* workspace, size_t workspace_bytes,
+                                 nvfp4_stream_t stream);
+nvfp4_status nvfp4_linear_epilogue(const void* x, int64_t m, int64_t k, int64_t ldx,
+                                   const float* x_global, const uint8_t* w_codes,
+                                   const uint8_t* w_sf, const float* w_global,
+                                   int64_t n, const void* bias,
+                                   nvfp4_activation activation, const void* residual,
+                                   int64_t ldr, void* y, int y_dtype, int64_t ldy,
+                                   void* workspace, size_t workspace_bytes,
+                                   nvfp4_stream_t stream);
+
 /*
  * nvfp4_gemm_swiglu_quant — gate_up projection of a W4A4 gated MLP with the
  * activation and the next layer's activation quantization fused into the

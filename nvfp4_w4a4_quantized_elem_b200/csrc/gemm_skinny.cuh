@@ -51,6 +51,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "epilogue.cuh"
 #include "fault.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -161,6 +162,7 @@ struct Params {
   const float* x_partials;
   int x_nparts;
   float* x_global_out;
+  epi::Args epi;            // EPI instantiation only
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
@@ -303,7 +305,7 @@ __device__ __forceinline__ void sum_slabs(const float* col, int64_t slab, int m0
   }
 }
 
-template <int BNT, bool FUSED>
+template <int BNT, bool FUSED, bool EPI>
 __global__ void __launch_bounds__(Cfg<BNT, FUSED>::THREADS, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const __grid_constant__ CUtensorMap tmSFW,
@@ -583,13 +585,29 @@ __global__ void __launch_bounds__(Cfg<BNT, FUSED>::THREADS, 1)
         n_contrib = cta_of(static_cast<int64_t>(wt + 1) * p.num_k_tiles - 1, T, gridDim.x) -
                     c_first + 1;
       }
+      const int nl = q * 32 + lane;            // column within the weight tile
+      const int n = wt * BW + nl;              // this thread's output column
+      const bool n_ok = n < p.N;
+      // EPI: this column's bias, and the residual of the tokens [m0, m0 + T)
+      // (bf16 bits; Y may be the residual, so every load of a group comes
+      // before its stores); the first group's loads do not wait for the sum
+      const float bias_n = EPI && p.epi.bias != nullptr && n_ok
+                               ? __bfloat162float(p.epi.bias[n]) : 0.0f;
+      auto load_res = [&](auto& rv, int m0) {
+        constexpr int T = static_cast<int>(sizeof(rv) / sizeof(rv[0]));
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+          rv[i] = p.epi.residual != nullptr && n_ok && m0 + i < p.M
+                      ? __bfloat162float(p.epi.residual[static_cast<int64_t>(m0 + i) * p.epi.ldr + n])
+                      : 0.0f;
+      };
+      constexpr int kGroup = BNT < 32 ? BNT : 32;  // tokens drained at a time
+      float res[EPI ? kGroup : 1];
+      if (EPI && whole) load_res(res, 0);
       if (!__all_sync(0xFFFFFFFFu, wait_bounded(&tmem_full[buf], (acc_phase >> buf) & 1u,
                                                 abort_flag, kFaultEpilogue, lim)))
         break;
       ptx::tc_fence_after();
-      const int nl = q * 32 + lane;            // column within the weight tile
-      const int n = wt * BW + nl;              // this thread's output column
-      const bool n_ok = n < p.N;
       const uint32_t lane_base =
           tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * static_cast<uint32_t>(BNT);
       // slab of this (tile, contributor): [M][BW]
@@ -607,6 +625,24 @@ __global__ void __launch_bounds__(Cfg<BNT, FUSED>::THREADS, 1)
         }
         ptx::tc_wait_ld();
         const int cols = BNT < 32 ? BNT : 32;
+        if (EPI && whole) {
+          if (c0 > 0) load_res(res, c0);
+          float z[kGroup];
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) z[i] = __uint_as_float(r[i]) * alpha + bias_n;
+          epi::activate_n(p.epi.act, z);
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) {
+            if (c0 + i >= p.M || !n_ok) continue;
+            const float v = z[i] + res[EPI ? i : 0];
+            const int64_t o = static_cast<int64_t>(c0 + i) * p.ldy + n;
+            if (p.y_fp32)
+              reinterpret_cast<float*>(p.y)[o] = v;
+            else
+              reinterpret_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+          }
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < cols; ++i) {
           const int m = c0 + i;                 // token
@@ -644,6 +680,8 @@ __global__ void __launch_bounds__(Cfg<BNT, FUSED>::THREADS, 1)
             constexpr int T = sum_tokens<BNT, FUSED>();
             for (int m0 = 0; m0 < p.M; m0 += T) {
               float acc[T];
+              float rs[EPI ? T : 1];
+              if (EPI) load_res(rs, m0);  // in the same round trip as the slabs
               switch (n_contrib) {
                 case 1: sum_slabs<1, T>(col, slab_len, m0, p.M, acc); break;
                 case 2: sum_slabs<2, T>(col, slab_len, m0, p.M, acc); break;
@@ -654,6 +692,13 @@ __global__ void __launch_bounds__(Cfg<BNT, FUSED>::THREADS, 1)
                 case 7: sum_slabs<7, T>(col, slab_len, m0, p.M, acc); break;
                 case 8: sum_slabs<8, T>(col, slab_len, m0, p.M, acc); break;
                 default: sum_slabs<kMaxContrib, T>(col, slab_len, m0, p.M, acc); break;
+              }
+              if (EPI) {
+#pragma unroll
+                for (int i = 0; i < T; ++i) acc[i] += bias_n;
+                epi::activate_n(p.epi.act, acc);
+#pragma unroll
+                for (int i = 0; i < T; ++i) acc[i] += rs[EPI ? i : 0];
               }
 #pragma unroll
               for (int i = 0; i < T; ++i) {

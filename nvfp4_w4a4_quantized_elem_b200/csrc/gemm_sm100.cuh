@@ -58,6 +58,13 @@
 // one max|h| per CTA, which the quantizer then reduces to h's global exactly
 // as it reduces the amax pass's partials: the output is that of the unfused
 // chain (GEMM -> bf16 gate/up -> silu*mul -> dynamic quantization of h).
+// Epilogue arguments (EPI instantiation, plain output only): bias, activation
+// and residual (epilogue.cuh) are applied to the FP32 accumulator, after the
+// slices' sum where K is split. The tile's bias is staged per warp in shared
+// memory before the accumulator is ready; a thread owns one output row, so
+// its residual comes in four 16-byte loads per 32 columns, behind the
+// accumulator's release and so beside the next tile's MMAs. A separate
+// instantiation: the plain kernel keeps its registers and its results.
 // Launched with programmatic stream serialisation: barrier set-up and
 // tensor-memory allocation overlap the previous kernel in the stream; the
 // producer and the epilogue wait for it before touching global memory, except
@@ -71,6 +78,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "epilogue.cuh"
 #include "fault.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -107,7 +115,11 @@ constexpr int EPI_WARP_BYTES = 2 * EPI_CHUNK_BYTES;
 constexpr int EPI_OFF = STAGES * STAGE_BYTES;  // staging tiles after the ring
 constexpr int BAR_OFF = EPI_OFF + NUM_EPI_WARPS * EPI_WARP_BYTES;
 constexpr int RTAB_OFF = BAR_OFF + 512;      // fused mode: g_h / dec(s) for 128 codes
-constexpr size_t SMEM_BYTES = 1024 + static_cast<size_t>(RTAB_OFF) + 512;
+constexpr int BIAS_OFF = RTAB_OFF + 512;     // EPI: 128 bf16 of bias per epilogue warp
+constexpr int BIAS_WARP_BYTES = 128 * 2;
+constexpr size_t SMEM_BYTES =
+    1024 + static_cast<size_t>(BIAS_OFF) + NUM_EPI_WARPS * BIAS_WARP_BYTES;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
 constexpr uint64_t kDrainLimitNs = 100000000ull;  // 0.1 s for the abort drain
 
@@ -154,6 +166,7 @@ struct Params {
   unsigned int* tile_count;   // [tiles][2 CTAs][8 regions], zero before and after
   int raster_n;               // bands of N-tiles (1) or of M-tiles (0)
   int group;                  // tiles per band (>= 1)
+  epi::Args epi;              // EPI instantiation only
 };
 
 enum : int { kPlain = 0, kFusedQuantStatic = 1, kFusedBf16Amax = 2 };
@@ -385,6 +398,7 @@ __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t ssfa, uint32
   }
 }
 
+template <bool EPI>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSFA,
@@ -642,7 +656,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // -------------------------------------------------------------- epilogue --
     ptx::grid_dep_wait();  // globals from earlier kernels; Y / h may still be in use
     float* rtab = reinterpret_cast<float*>(smem + RTAB_OFF);
-    if (p.fused == kFusedQuantStatic) {
+    if (!EPI && p.fused == kFusedQuantStatic) {
       // E4M3 code -> g_h / dec(code), as the quantizer tabulates it
       const float gh = __ldg(p.h_global);
       const int t = threadIdx.x - EPI_WARP0 * 32;
@@ -679,11 +693,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Unit unit = unit_of(t, p);
       int mb, nb;
       tile_coords(unit.tile, p, mb, nb);
+      uint16_t* const bias_tile = reinterpret_cast<uint16_t*>(
+          smem + BIAS_OFF + (warp - EPI_WARP0) * BIAS_WARP_BYTES);
+      if (EPI && p.epi.bias != nullptr) {  // this warp's 128 columns, 4 per lane
+        const int c0 = nb * BN + half * 128 + 4 * lane;
+        const uint16_t* b = reinterpret_cast<const uint16_t*>(p.epi.bias) + c0;
+        uint32_t w0 = 0u, w1 = 0u;
+        if (c0 + 4 <= p.N) {
+          const uint2 v = *reinterpret_cast<const uint2*>(b);
+          w0 = v.x;
+          w1 = v.y;
+        } else {
+          if (c0 < p.N) w0 = b[0];
+          if (c0 + 1 < p.N) w0 |= static_cast<uint32_t>(b[1]) << 16;
+          if (c0 + 2 < p.N) w1 = b[2];
+        }
+        __syncwarp();  // the previous tile's reads are over
+        reinterpret_cast<uint2*>(bias_tile)[lane] = make_uint2(w0, w1);
+        __syncwarp();
+      }
       // warp-uniform: no lane may leave while the others go on to the
       // warp-wide tensor-memory loads
       if (!__all_sync(0xFFFFFFFFu, wait_bounded(tmem_full, acc_phase, ab, kFaultEpilogue))) break;
       ptx::tc_fence_after();
-      if (p.fused == kFusedBf16Amax) {
+      if (!EPI && p.fused == kFusedBf16Amax) {
         // gate columns [64 half, +64) and the matching up columns (+128) ->
         // 64 bf16 h columns of 32 rows, two TMA-stored chunks
         uint32_t g0[32], g1[32], u0[32], u1[32];
@@ -704,7 +737,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         emit([&](uint32_t b) { stage_h(b, lane, g1, u1, alpha, h_amax); }, hc0 + 32, row0);
         continue;
       }
-      if (p.fused == kFusedQuantStatic) {
+      if (!EPI && p.fused == kFusedQuantStatic) {
         // gate columns [64 half, +64) and the matching up columns (+128)
         uint32_t g0[32], g1[32], u0[32], u1[32];
         const uint32_t lb = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64u * half;
@@ -752,6 +785,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
       const int row0 = mb * BM + static_cast<int>(rank) * HALF + q * 32;  // this warp's rows
       const int col0 = nb * BN + half * 128;
+      // EPI: columns [32 cc, +32) of this thread's row, in place; alpha is then spent
+      const __nv_bfloat16* res_row = nullptr;
+      if (EPI && p.epi.residual != nullptr && row0 + lane < p.M)
+        res_row = p.epi.residual + static_cast<int64_t>(row0 + lane) * p.epi.ldr + col0;
+      auto finish = [&](uint32_t(&acc)[32], int cc) {
+        epi::apply32(acc, alpha, p.epi.act,
+                     p.epi.bias != nullptr ? bias_tile + 32 * cc : nullptr,
+                     res_row != nullptr ? res_row + 32 * cc : nullptr, p.N - col0 - 32 * cc);
+      };
+      const float beta = EPI ? 1.0f : alpha;  // scale left to the staging
       if (p.split > 1) {
         // rows past M (a tile's padding): no partial, no count, no output
         if (row0 >= p.M) continue;
@@ -794,11 +837,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             case 3: sum_slices<3>(src, slab_stride / 4, acc); break;
             default: sum_slices<kMaxSplitK>(src, slab_stride / 4, acc); break;
           }
+          if (EPI) finish(acc, cc);
           if (!p.y_fp32) {
-            emit([&](uint32_t b) { stage_bf16(b, lane, acc, alpha); }, col0 + 32 * cc, row0);
+            emit([&](uint32_t b) { stage_bf16(b, lane, acc, beta); }, col0 + 32 * cc, row0);
           } else {
-            emit([&](uint32_t b) { stage_f32(b, lane, acc, 0, alpha); }, col0 + 32 * cc, row0);
-            emit([&](uint32_t b) { stage_f32(b, lane, acc, 16, alpha); }, col0 + 32 * cc + 16,
+            emit([&](uint32_t b) { stage_f32(b, lane, acc, 0, beta); }, col0 + 32 * cc, row0);
+            emit([&](uint32_t b) { stage_f32(b, lane, acc, 16, beta); }, col0 + 32 * cc + 16,
                  row0);
           }
         }
@@ -806,24 +850,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         continue;
       }
       if (row0 >= p.M) continue;  // warp-uniform; rows past M inside are clipped by the TMA
-      if (!p.y_fp32) {
-        emit([&](uint32_t b) { stage_bf16(b, lane, r0, alpha); }, col0 + 0, row0);
-        emit([&](uint32_t b) { stage_bf16(b, lane, r1, alpha); }, col0 + 32, row0);
-        emit([&](uint32_t b) { stage_bf16(b, lane, r2, alpha); }, col0 + 64, row0);
-        emit([&](uint32_t b) { stage_bf16(b, lane, r3, alpha); }, col0 + 96, row0);
-      } else {
-        emit([&](uint32_t b) { stage_f32(b, lane, r0, 0, alpha); }, col0 + 0, row0);
-        emit([&](uint32_t b) { stage_f32(b, lane, r0, 16, alpha); }, col0 + 16, row0);
-        emit([&](uint32_t b) { stage_f32(b, lane, r1, 0, alpha); }, col0 + 32, row0);
-        emit([&](uint32_t b) { stage_f32(b, lane, r1, 16, alpha); }, col0 + 48, row0);
-        emit([&](uint32_t b) { stage_f32(b, lane, r2, 0, alpha); }, col0 + 64, row0);
-        emit([&](uint32_t b) { stage_f32(b, lane, r2, 16, alpha); }, col0 + 80, row0);
-        emit([&](uint32_t b) { stage_f32(b, lane, r3, 0, alpha); }, col0 + 96, row0);
-        emit([&](uint32_t b) { stage_f32(b, lane, r3, 16, alpha); }, col0 + 112, row0);
-      }
+      auto put = [&](uint32_t(&acc)[32], int cc) {
+        if (EPI) finish(acc, cc);
+        if (!p.y_fp32) {
+          emit([&](uint32_t b) { stage_bf16(b, lane, acc, beta); }, col0 + 32 * cc, row0);
+        } else {
+          emit([&](uint32_t b) { stage_f32(b, lane, acc, 0, beta); }, col0 + 32 * cc, row0);
+          emit([&](uint32_t b) { stage_f32(b, lane, acc, 16, beta); }, col0 + 32 * cc + 16, row0);
+        }
+      };
+      put(r0, 0);
+      put(r1, 1);
+      put(r2, 2);
+      put(r3, 3);
     }
     if (lane == 0) ptx::bulk_wait_group_all();  // stores done before the CTA can exit
-    if (p.fused == kFusedBf16Amax) {
+    if (!EPI && p.fused == kFusedBf16Amax) {
       // one partial max per CTA (order-free, so the global that the
       // quantizer derives from the partials does not depend on timing);
       // every epilogue warp gets here, also after an abort

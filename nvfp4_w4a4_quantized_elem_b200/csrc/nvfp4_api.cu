@@ -19,6 +19,7 @@
 #include <mutex>
 #include <utility>
 
+#include "epilogue.cuh"
 #include "fold.cuh"
 #include "gemm_sm100.cuh"
 #include "gemm_skinny.cuh"
@@ -41,7 +42,7 @@ constexpr int kMaxDevices = 64;
 struct DeviceState {
   unsigned long long ctx_id = 0;      // context the fields below belong to (0 = none yet)
   int sms = 0;
-  bool gemm_smem_set = false;
+  unsigned gemm_smem_set = 0;         // bit per instantiation (plain, epilogue)
   unsigned skinny_smem_set = 0;       // bit per token-tile instantiation
   int amax_per_sm = 0;                // resident CTAs per SM of the quantizer's kernels
   int quant_per_sm = 0;
@@ -531,15 +532,15 @@ nvfp4_status encode_sf(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, 
   return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
-template <int BNT, bool FUSED>
-nvfp4_status launch_skinny(DeviceState* st, int bit, const CUtensorMap& tmW, const CUtensorMap& tmX,
+template <int BNT, bool FUSED, bool EPI>
+nvfp4_status launch_skinny_as(DeviceState* st, int bit, const CUtensorMap& tmW, const CUtensorMap& tmX,
                            const CUtensorMap& tmSFW, const CUtensorMap& tmSFX,
                            const nvfp4::skinny::Params& p, int grid, cudaStream_t s) {
   using C = nvfp4::skinny::Cfg<BNT, FUSED>;
   {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (!(st->skinny_smem_set & (1u << bit))) {
-      if (cudaFuncSetAttribute(nvfp4::skinny::skinny_kernel<BNT, FUSED>,
+      if (cudaFuncSetAttribute(nvfp4::skinny::skinny_kernel<BNT, FUSED, EPI>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(C::SMEM_BYTES)) != cudaSuccess) {
         cudaGetLastError();
@@ -548,8 +549,22 @@ nvfp4_status launch_skinny(DeviceState* st, int bit, const CUtensorMap& tmW, con
       st->skinny_smem_set |= 1u << bit;
     }
   }
-  return launch_pdl(nvfp4::skinny::skinny_kernel<BNT, FUSED>, static_cast<unsigned>(grid),
+  return launch_pdl(nvfp4::skinny::skinny_kernel<BNT, FUSED, EPI>, static_cast<unsigned>(grid),
                     C::THREADS, C::SMEM_BYTES, s, 1u, tmW, tmX, tmSFW, tmSFX, p);
+}
+
+// Whether a call's epilogue does anything (else the plain kernel runs).
+bool has_epilogue(const nvfp4::epi::Args& e) {
+  return e.bias != nullptr || e.residual != nullptr || e.act != nvfp4::epi::kNone;
+}
+
+template <int BNT, bool FUSED>
+nvfp4_status launch_skinny(DeviceState* st, int bit, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                           const CUtensorMap& tmSFW, const CUtensorMap& tmSFX,
+                           const nvfp4::skinny::Params& p, int grid, cudaStream_t s) {
+  return has_epilogue(p.epi)
+             ? launch_skinny_as<BNT, FUSED, true>(st, bit + 4, tmW, tmX, tmSFW, tmSFX, p, grid, s)
+             : launch_skinny_as<BNT, FUSED, false>(st, bit, tmW, tmX, tmSFW, tmSFX, p, grid, s);
 }
 
 // Tokens quantized inside the few-token GEMM (nvfp4_linear, m <= XR = 8): the
@@ -577,7 +592,7 @@ nvfp4_status gemm_skinny(PFN_cuTensorMapEncodeTiled_v12000 enc, DeviceState* st,
                          void* y, int y_dtype, int64_t ldy, int64_t m, int64_t n, int64_t k,
                          void* workspace, size_t workspace_bytes, bool zero_counters,
                          int early_w, cudaStream_t s, int stall = 0, uint64_t limit_ns = 0,
-                         const XFused* xf = nullptr) {
+                         const XFused* xf = nullptr, const nvfp4::epi::Args& ep = {}) {
   using namespace nvfp4::skinny;
   const int bnt = m <= 16 ? 16 : m <= 32 ? 32 : 64;  // callers route m <= 64 here
   if (xf != nullptr && m > XR) return NVFP4_ERR_UNSUPPORTED;
@@ -629,6 +644,7 @@ nvfp4_status gemm_skinny(PFN_cuTensorMapEncodeTiled_v12000 enc, DeviceState* st,
   p.stream_k = 0;
   p.stall_first_stage = stall;
   p.wait_limit_ns = limit_ns;
+  p.epi = ep;
   int grid = static_cast<int>(p.num_w_tiles < st->sms ? p.num_w_tiles : st->sms);
   const bool split_ok = workspace != nullptr &&
                         workspace_bytes >= skinny_workspace_bytes(m, n) && aligned(workspace, 16);
@@ -686,15 +702,18 @@ nvfp4_status gemm_paired(PFN_cuTensorMapEncodeTiled_v12000 enc, DeviceState* st,
   } else if (p.fused == kFusedBf16Amax) {  // bf16 h = [m][n / 2]
     if (nvfp4_status e = encode_y(enc, &tmY, p.y, m, n / 2, p.ldy, 0)) return e;
   }
+  const bool ep = has_epilogue(p.epi);
+  const auto kernel = ep ? gemm_kernel<true> : gemm_kernel<false>;
   {
     std::lock_guard<std::mutex> lock(g_mutex);
-    if (!st->gemm_smem_set) {
-      if (cudaFuncSetAttribute(gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const unsigned bit = ep ? 2u : 1u;
+    if (!(st->gemm_smem_set & bit)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(SMEM_BYTES)) != cudaSuccess) {
         cudaGetLastError();
         return NVFP4_ERR_CUDA;
       }
-      st->gemm_smem_set = true;
+      st->gemm_smem_set |= bit;
     }
   }
   p.M = static_cast<int>(m);
@@ -746,16 +765,58 @@ nvfp4_status gemm_paired(PFN_cuTensorMapEncodeTiled_v12000 enc, DeviceState* st,
   const int64_t max_pairs = st->sms / 2;
   const int pairs = static_cast<int>(units < max_pairs ? units : max_pairs);
   if (grid_out != nullptr) *grid_out = 2 * pairs;
-  return launch_pdl(gemm_kernel, static_cast<unsigned>(2 * pairs), NUM_THREADS, SMEM_BYTES,
+  return launch_pdl(kernel, static_cast<unsigned>(2 * pairs), NUM_THREADS, SMEM_BYTES,
                     stream, 2u, tmA, tmB, tmSFA, tmSFB, tmY, p);
 }
 
-// nvfp4_gemm; `stall` / `limit_ns` only for nvfp4_selftest_gemm_stall.
+// Checks of an epilogue's arguments against the output they go with.
+// Y may be the residual itself (the same rows in place: every element is
+// read before it is written, by the thread that writes it), or the two may be
+// disjoint columns of one matrix; any other overlap is refused.
+nvfp4_status check_epilogue(const void* bias, int activation, const void* residual, int64_t ldr,
+                            const void* y, int y_dtype, int64_t ldy, int64_t m, int64_t n) {
+  if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_GELU_TANH) return NVFP4_ERR_INVALID_ARG;
+  const int64_t esize = y_dtype == 0 ? 2 : 4;
+  const uintptr_t y0 = reinterpret_cast<uintptr_t>(y);
+  const uintptr_t y1 = y0 + static_cast<uintptr_t>(((m - 1) * ldy + n) * esize);
+  if (bias != nullptr) {
+    if (!aligned(bias, 16)) return NVFP4_ERR_MISALIGNED;
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(bias);
+    if (b0 < y1 && y0 < b0 + static_cast<uintptr_t>(n) * 2) return NVFP4_ERR_INVALID_ARG;
+  }
+  if (residual != nullptr) {
+    if (ldr < n) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(residual, 16) || ldr % 8 != 0) return NVFP4_ERR_MISALIGNED;
+    const uintptr_t r0 = reinterpret_cast<uintptr_t>(residual);
+    if (r0 < y1 && y0 < r0 + static_cast<uintptr_t>(((m - 1) * ldr + n) * 2)) {
+      if (y_dtype != 0 || (m > 1 && ldr != ldy)) return NVFP4_ERR_INVALID_ARG;
+      if (m == 1 && r0 != y0) return NVFP4_ERR_INVALID_ARG;  // one row: no pitch to be disjoint by
+      const int64_t d = (static_cast<int64_t>(r0) - static_cast<int64_t>(y0)) / 2;
+      const int64_t c = ((d % ldy) + ldy) % ldy;  // the residual's column offset
+      if (d != 0 && (c < n || ldy - c < n)) return NVFP4_ERR_INVALID_ARG;
+    }
+  }
+  return NVFP4_OK;
+}
+
+nvfp4::epi::Args epilogue_args(const void* bias, int activation, const void* residual,
+                               int64_t ldr) {
+  nvfp4::epi::Args e;
+  e.bias = static_cast<const __nv_bfloat16*>(bias);
+  e.residual = static_cast<const __nv_bfloat16*>(residual);
+  e.ldr = ldr;
+  e.act = activation;
+  return e;
+}
+
+// nvfp4_gemm and nvfp4_gemm_epilogue; `stall` / `limit_ns` only for
+// nvfp4_selftest_gemm_stall.
 nvfp4_status gemm_entry(const uint8_t* a_codes, const uint8_t* a_sf, const float* a_global,
                         const uint8_t* b_codes, const uint8_t* b_sf, const float* b_global,
                         void* y, int y_dtype, int64_t ldy, int64_t m, int64_t n, int64_t k,
                         void* workspace, size_t workspace_bytes, nvfp4_stream_t stream,
-                        int stall, uint64_t limit_ns) {
+                        int stall, uint64_t limit_ns, const void* bias = nullptr,
+                        int activation = 0, const void* residual = nullptr, int64_t ldr = 0) {
   using namespace nvfp4::gemm;
   if (!a_codes || !a_sf || !a_global || !b_codes || !b_sf || !b_global || !y)
     return NVFP4_ERR_INVALID_ARG;
@@ -768,6 +829,9 @@ nvfp4_status gemm_entry(const uint8_t* a_codes, const uint8_t* a_sf, const float
   if (!aligned(a_codes, 16) || !aligned(b_codes, 16) || !aligned(a_sf, 16) || !aligned(b_sf, 16) ||
       !aligned(y, 16) || (ldy * esize) % 16 != 0 || !aligned(a_global, 4) || !aligned(b_global, 4))
     return NVFP4_ERR_MISALIGNED;
+  if (nvfp4_status e = check_epilogue(bias, activation, residual, ldr, y, y_dtype, ldy, m, n))
+    return e;
+  const nvfp4::epi::Args ep = epilogue_args(bias, activation, residual, ldr);
   int dev;
   DeviceState* st;
   if (nvfp4_status e = current_device(&dev, &st)) return e;
@@ -776,7 +840,7 @@ nvfp4_status gemm_entry(const uint8_t* a_codes, const uint8_t* a_sf, const float
   if (m <= 64)
     return gemm_skinny(enc, st, a_codes, a_sf, a_global, b_codes, b_sf, b_global, y, y_dtype, ldy,
                        m, n, k, workspace, workspace_bytes, true, 0,
-                       reinterpret_cast<cudaStream_t>(stream), stall, limit_ns);
+                       reinterpret_cast<cudaStream_t>(stream), stall, limit_ns, nullptr, ep);
 
   nvfp4::gemm::Params p;
   std::memset(&p, 0, sizeof p);
@@ -787,6 +851,7 @@ nvfp4_status gemm_entry(const uint8_t* a_codes, const uint8_t* a_sf, const float
   p.y_fp32 = y_dtype;
   p.stall_first_stage = stall;
   p.wait_limit_ns = limit_ns;
+  p.epi = ep;
   return gemm_paired(enc, st, a_codes, a_sf, b_codes, b_sf, m, n, k, p,
                      reinterpret_cast<cudaStream_t>(stream), nullptr, workspace, workspace_bytes,
                      true);
@@ -828,10 +893,16 @@ size_t nvfp4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   return b;
 }
 
-nvfp4_status nvfp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx,
+}  // extern "C"
+
+namespace {
+
+// nvfp4_linear and nvfp4_linear_epilogue.
+nvfp4_status linear_entry(const void* x, int64_t m, int64_t k, int64_t ldx,
                           const float* x_global, const uint8_t* w_codes, const uint8_t* w_sf,
                           const float* w_global, int64_t n, void* y, int y_dtype, int64_t ldy,
-                          void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
+                          void* workspace, size_t workspace_bytes, nvfp4_stream_t stream, const void* bias = nullptr,
+                          int activation = 0, const void* residual = nullptr, int64_t ldr = 0) {
   if (!x || !w_codes || !w_sf || !w_global || !y || !workspace) return NVFP4_ERR_INVALID_ARG;
   if (m < 1 || n < 1 || k < 1 || (y_dtype != 0 && y_dtype != 1) || ldy < n || ldx < k)
     return NVFP4_ERR_INVALID_ARG;
@@ -844,6 +915,9 @@ nvfp4_status nvfp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx,
       !aligned(x_global, 4) || !aligned(workspace, 256))
     return NVFP4_ERR_MISALIGNED;
   if (workspace_bytes < nvfp4_linear_workspace_bytes(m, n, k)) return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status e = check_epilogue(bias, activation, residual, ldr, y, y_dtype, ldy, m, n))
+    return e;
+  const nvfp4::epi::Args ep = epilogue_args(bias, activation, residual, ldr);
   int dev;
   DeviceState* st;
   if (nvfp4_status e = current_device(&dev, &st)) return e;
@@ -881,7 +955,7 @@ nvfp4_status nvfp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx,
       xf.nparts = static_cast<int>(blocks);
     }
     return gemm_skinny(enc, st, a_codes, a_sf, a_global, w_codes, w_sf, w_global, y, y_dtype, ldy,
-                       m, n, k, w, skinny_workspace_bytes(m, n), false, 1, s, 0, 0, &xf);
+                       m, n, k, w, skinny_workspace_bytes(m, n), false, 1, s, 0, 0, &xf, ep);
   }
   // the quantized X is private to this call: its padding rows' scales are
   // not written (only the GEMM reads them, against zero-filled codes)
@@ -890,7 +964,7 @@ nvfp4_status nvfp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx,
     return e;
   if (m <= 64)
     return gemm_skinny(enc, st, a_codes, a_sf, a_global, w_codes, w_sf, w_global, y, y_dtype, ldy,
-                       m, n, k, w, skinny_workspace_bytes(m, n), false, 1, s);
+                       m, n, k, w, skinny_workspace_bytes(m, n), false, 1, s, 0, 0, nullptr, ep);
   nvfp4::gemm::Params p;
   std::memset(&p, 0, sizeof p);
   p.a_global = a_global;
@@ -899,8 +973,43 @@ nvfp4_status nvfp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx,
   p.ldy = ldy;
   p.y_fp32 = y_dtype;
   p.early_w = 1;
+  p.epi = ep;
   return gemm_paired(enc, st, a_codes, a_sf, w_codes, w_sf, m, n, k, p, s, nullptr,
                      split_bytes ? w : nullptr, split_bytes, false);
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a_codes, const uint8_t* a_sf,
+                                 const float* a_global, const uint8_t* b_codes,
+                                 const uint8_t* b_sf, const float* b_global, const void* bias,
+                                 nvfp4_activation activation, const void* residual, int64_t ldr,
+                                 void* y, int y_dtype, int64_t ldy, int64_t m, int64_t n,
+                                 int64_t k, void* workspace, size_t workspace_bytes,
+                                 nvfp4_stream_t stream) {
+  return gemm_entry(a_codes, a_sf, a_global, b_codes, b_sf, b_global, y, y_dtype, ldy, m, n, k,
+                    workspace, workspace_bytes, stream, 0, 0, bias, activation, residual, ldr);
+}
+
+nvfp4_status nvfp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx,
+                          const float* x_global, const uint8_t* w_codes, const uint8_t* w_sf,
+                          const float* w_global, int64_t n, void* y, int y_dtype, int64_t ldy,
+                          void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
+  return linear_entry(x, m, k, ldx, x_global, w_codes, w_sf, w_global, n, y, y_dtype, ldy,
+                      workspace, workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_linear_epilogue(const void* x, int64_t m, int64_t k, int64_t ldx,
+                                   const float* x_global, const uint8_t* w_codes,
+                                   const uint8_t* w_sf, const float* w_global, int64_t n,
+                                   const void* bias, nvfp4_activation activation,
+                                   const void* residual, int64_t ldr, void* y, int y_dtype,
+                                   int64_t ldy, void* workspace, size_t workspace_bytes,
+                                   nvfp4_stream_t stream) {
+  return linear_entry(x, m, k, ldx, x_global, w_codes, w_sf, w_global, n, y, y_dtype, ldy,
+                      workspace, workspace_bytes, stream, bias, activation, residual, ldr);
 }
 
 nvfp4_status nvfp4_gemm_swiglu_quant(const uint8_t* a_codes, const uint8_t* a_sf,

@@ -32,10 +32,14 @@ STATUS_NAMES = {0: "NVFP4_OK", 1: "NVFP4_ERR_INVALID_ARG", 2: "NVFP4_ERR_UNSUPPO
 EXPORTS = ("nvfp4_status_string", "nvfp4_sf_bytes", "nvfp4_quantize_workspace_bytes",
            "nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_calibrate_global",
            "nvfp4_gemm_workspace_bytes", "nvfp4_gemm", "nvfp4_linear_workspace_bytes",
-           "nvfp4_linear", "nvfp4_gemm_swiglu_quant",
+           "nvfp4_linear", "nvfp4_gemm_epilogue", "nvfp4_linear_epilogue",
+           "nvfp4_gemm_swiglu_quant",
            "nvfp4_gemm_swiglu_quant_dynamic_workspace_bytes", "nvfp4_gemm_swiglu_quant_dynamic",
            "nvfp4_fuse_group_scales", "nvfp4_silu_mul", "nvfp4_read_fault",
            "nvfp4_selftest_wait_timeout", "nvfp4_selftest_gemm_stall")
+
+# activations of the GEMM epilogue (nvfp4_activation)
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 _lib = None
 _lock = threading.Lock()
@@ -71,6 +75,10 @@ def lib() -> ctypes.CDLL:
             "nvfp4_gemm": (I, [P, P, P, P, P, P, P, I, I64, I64, I64, I64, P, SZ, P]),
             "nvfp4_linear_workspace_bytes": (SZ, [I64, I64, I64]),
             "nvfp4_linear": (I, [P, I64, I64, I64, P, P, P, P, I64, P, I, I64, P, SZ, P]),
+            "nvfp4_gemm_epilogue": (I, [P, P, P, P, P, P, P, I, P, I64, P, I, I64, I64, I64, I64,
+                                        P, SZ, P]),
+            "nvfp4_linear_epilogue": (I, [P, I64, I64, I64, P, P, P, P, I64, P, I, P, I64, P, I,
+                                          I64, P, SZ, P]),
             "nvfp4_gemm_swiglu_quant": (I, [P, P, P, P, P, P, P, P, P, I64, I64, I64, P]),
             "nvfp4_gemm_swiglu_quant_dynamic_workspace_bytes": (SZ, [I64, I64]),
             "nvfp4_gemm_swiglu_quant_dynamic": (I, [P, P, P, P, P, P, P, P, P, I64, I64, I64,
@@ -201,17 +209,42 @@ class Calibrator:
         return self.global_scale
 
 
+def _epilogue(bias: torch.Tensor | None, activation: str, residual: torch.Tensor | None,
+              m: int, n: int, device: torch.device):
+    """Checked epilogue arguments: (bias pointer, activation code, residual
+    pointer, residual row pitch)."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    for t, name in ((bias, "bias"), (residual, "residual")):
+        if t is not None:
+            _require_cuda(t, name, torch.bfloat16)
+            if t.device != device:
+                raise ValueError(f"{name} must be on {device}")
+    if bias is not None and (tuple(bias.shape) != (n,) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous vector of {n}")
+    ldr = 0
+    if residual is not None:
+        if tuple(residual.shape) != (m, n) or (n > 1 and residual.stride(1) != 1):
+            raise ValueError(f"residual must be [{m}, {n}] with unit column stride")
+        # a single row's pitch is free; a C caller may give any valid one
+        ldr = residual.stride(0) if m > 1 else -(-n // 8) * 8
+    return _ptr(bias), ACTIVATIONS[activation], _ptr(residual), ldr
+
+
 def gemm_workspace_bytes(m: int, n: int, k: int) -> int:
     return int(lib().nvfp4_gemm_workspace_bytes(m, n, k))
 
 
 def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out: torch.Tensor | None = None,
          out_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None,
-         stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+         stream: torch.cuda.Stream | None = None, bias: torch.Tensor | None = None,
+         activation: str = "none", residual: torch.Tensor | None = None) -> torch.Tensor:
     """nvfp4_gemm: Y[m, n] = dequant(A) @ dequant(B).T (A = activations
     [m, k], B = weights [n, k]); bf16 or fp32 output. ``workspace`` (at least
     gemm_workspace_bytes) lets few-token GEMMs share the work across all SMs
-    (stream-K)."""
+    (stream-K). With ``bias`` (bf16 [n]), ``activation`` (a key of ACTIVATIONS)
+    or ``residual`` (bf16 [m, n], may be ``out``): nvfp4_gemm_epilogue,
+    Y = act(product + bias) + residual in FP32, rounded once."""
     if a.k != b.k:
         raise ValueError("k mismatch")
     m, n, k = a.rows, b.rows, a.k
@@ -221,6 +254,14 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out: torch.Tensor | None = None,
         raise ValueError("out must be bf16/fp32 with unit column stride")
     y_dtype = 0 if out.dtype == torch.bfloat16 else 1
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if bias is not None or residual is not None or activation != "none":
+        st = lib().nvfp4_gemm_epilogue(
+            _ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale), _ptr(b.codes), _ptr(b.sf),
+            _ptr(b.global_scale), *_epilogue(bias, activation, residual, m, n, out.device),
+            _ptr(out), y_dtype, out.stride(0), m, n, k, _ptr(workspace), ws_bytes,
+            _stream(stream))
+        _check(st, "nvfp4_gemm_epilogue")
+        return out
     st = lib().nvfp4_gemm(_ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale),
                           _ptr(b.codes), _ptr(b.sf), _ptr(b.global_scale),
                           _ptr(out), y_dtype, out.stride(0), m, n, k, _ptr(workspace), ws_bytes,
@@ -383,11 +424,15 @@ def linear_workspace(m: int, n: int, k: int, device="cuda") -> torch.Tensor:
 def linear(x: torch.Tensor, w: NVFP4Tensor, out: torch.Tensor | None = None,
            out_dtype: torch.dtype = torch.bfloat16, global_scale: torch.Tensor | None = None,
            workspace: torch.Tensor | None = None,
-           stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+           stream: torch.cuda.Stream | None = None, bias: torch.Tensor | None = None,
+           activation: str = "none", residual: torch.Tensor | None = None) -> torch.Tensor:
     """nvfp4_linear, the W4A4 linear layer in one call: quantize x (dynamic
     global, or the static ``global_scale``) and multiply with the NVFP4
     weights ``w`` [n, k]; the GEMM's launch overlaps the quantization.
-    ``workspace`` from linear_workspace() (allocated here when None)."""
+    ``workspace`` from linear_workspace() (allocated here when None).
+    With ``bias`` (bf16 [n]), ``activation`` (a key of ACTIVATIONS) or
+    ``residual`` (bf16 [m, n], may be ``out``): nvfp4_linear_epilogue,
+    Y = act(product + bias) + residual in FP32, rounded once."""
     _require_cuda(x, "x", torch.bfloat16)
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit stride along k")
@@ -401,6 +446,14 @@ def linear(x: torch.Tensor, w: NVFP4Tensor, out: torch.Tensor | None = None,
         raise ValueError("out must be bf16/fp32 with unit column stride")
     if workspace is None:
         workspace = linear_workspace(m, n, k, x.device)
+    if bias is not None or residual is not None or activation != "none":
+        st = lib().nvfp4_linear_epilogue(
+            _ptr(x), m, k, x.stride(0), _ptr(global_scale), _ptr(w.codes), _ptr(w.sf),
+            _ptr(w.global_scale), n, *_epilogue(bias, activation, residual, m, n, out.device),
+            _ptr(out), 0 if out.dtype == torch.bfloat16 else 1, out.stride(0), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+        _check(st, "nvfp4_linear_epilogue")
+        return out
     st = lib().nvfp4_linear(_ptr(x), m, k, x.stride(0), _ptr(global_scale), _ptr(w.codes),
                             _ptr(w.sf), _ptr(w.global_scale), n, _ptr(out),
                             0 if out.dtype == torch.bfloat16 else 1, out.stride(0),

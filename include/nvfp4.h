@@ -438,6 +438,88 @@ nvfp4_status nvfp4_fuse_group_scales(int n_modules,
 nvfp4_status nvfp4_silu_mul(const void* y, int64_t m, int64_t n, int64_t ldy,
                             void* h, int64_t ldh, nvfp4_stream_t stream);
 
+/* Workspace bytes of nvfp4_linear_attention: per 64-token chunk slot (at most
+ * total/64 + n_seq) an image of the keys and queries for every key head and of
+ * the chunk's 64x64 factors for every value head. 0 for invalid sizes. */
+size_t nvfp4_linear_attention_workspace_bytes(int64_t total, int64_t n_seq, int h_k,
+                                              int h_v, int d_k);
+
+/*
+ * nvfp4_linear_attention — linear attention with a decay for each head over
+ * packed prompts: the recurrence of the Gated DeltaNet layers that the W4A4
+ * input projections feed (news §01 names the gated delta rule; its formula did
+ * not survive extraction, this is the Gated DeltaNet form its text describes).
+ * Per sequence and value head, from the state S [d_k][d_v]:
+ *   S <- e^g S;  u = beta (v - S^T k)  or, with beta NULL, u = v;
+ *   S <- S + k u^T;  o = scale * S^T q
+ * for one token after the other, computed in chunks of 64 tokens on the tensor
+ * cores with S in FP32.
+ *   q, k       device bf16 [total][ld]; head i of h_k at columns [i d_k, +d_k).
+ *   v          device bf16 [total][ldv]; head i of h_v at columns [i d_v, +d_v).
+ *              Value head i goes with key head i / (h_v / h_k). q, k and v may
+ *              be column ranges of one fused projection.
+ *   decay      device FP32 [total][h_v]: g, the log of the decay (g <= 0; -inf
+ *              or anything below -1000 forgets the state).
+ *   beta       device FP32 [total][h_v] or NULL. The delta rule is stable for
+ *              beta |k|^2 <= 2; the keys are taken as they are (not normalised).
+ *   total      packed tokens, >= 0.   n_seq >= 1 sequences:
+ *   cu_seqlens device int32 [n_seq + 1], non-decreasing from 0: sequence i is
+ *              rows [cu[i], cu[i+1]), of any length from 0. Rows behind the
+ *              last sequence are not read and their o stays as it was. Offsets
+ *              outside [0, total] are cut to it. NULL: one sequence of total.
+ *   state      device FP32 [n_slots][h_v][d_k][d_v] or NULL: the pool that
+ *              nvfp4_linear_attention_step continues. Each sequence's final
+ *              state is written to its slot (with NULL nowhere).
+ *   slots      device int32 [n_seq] or NULL (sequence i uses slot i; n_slots >=
+ *              n_seq). A sequence whose slot lies outside the pool, or is named
+ *              by an earlier sequence of the call, has none: it starts from
+ *              zero and its final state is dropped.
+ *   resume     device int32 [n_seq] or NULL: sequence i starts from its slot's
+ *              state where resume[i] != 0, else (and with NULL) from zero.
+ *   o          device bf16 [total][ldo]; must not overlap an input (other
+ *              columns of an input's matrix are allowed).
+ *   workspace  device scratch, 256-byte aligned, of
+ *              nvfp4_linear_attention_workspace_bytes(...) bytes, owned by the
+ *              caller, not shared with a call that may run at the same time; no
+ *              initialisation needed.
+ *   h_v % h_k == 0; d_k 64 or 128; d_v % 32 == 0; all row pitches multiples of
+ *   8 elements; q, k, v, o, state 16-byte aligned.
+ * Two kernels. The MMA operands made from FP32 values (states, the chunk's
+ * factors) are split into two bf16 pieces each: states and outputs carry
+ * errors of about 2^-17 of their scale before o's rounding to bf16.
+ * Results do not depend on the run or on the other sequences of the call.
+ * Errors: INVALID_ARG, UNSUPPORTED (d_k, d_v, sizes >= 2^31), MISALIGNED, CUDA.
+ */
+nvfp4_status nvfp4_linear_attention(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                    const void* v, int64_t ldv, const float* decay,
+                                    const float* beta, float scale, int64_t total, int h_k,
+                                    int h_v, int d_k, int d_v, int64_t n_seq,
+                                    const int32_t* cu_seqlens, float* state,
+                                    int64_t n_slots, const int32_t* slots,
+                                    const int32_t* resume, void* o, int64_t ldo,
+                                    void* workspace, size_t workspace_bytes,
+                                    nvfp4_stream_t stream);
+
+/*
+ * nvfp4_linear_attention_step — the same recurrence for one token per row, the
+ * decode step: row i of q, k, v, decay, beta advances the state in slots[i]
+ * (NULL: slot i; n_slots >= batch) in place and gives row i of o. All in FP32
+ * (no tensor cores), o rounded to bf16.
+ *   A row whose slot lies outside the pool is padding: nothing of it is read
+ *   and its o stays as it was. Rows that name the same slot are taken in row
+ *   order (several tokens of one sequence).
+ *   All other arguments as nvfp4_linear_attention; state is required; batch 0
+ *   does nothing. One kernel, no workspace.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA.
+ */
+nvfp4_status nvfp4_linear_attention_step(const void* q, int64_t ldq, const void* k,
+                                         int64_t ldk, const void* v, int64_t ldv,
+                                         const float* decay, const float* beta,
+                                         float scale, int64_t batch, int h_k, int h_v,
+                                         int d_k, int d_v, float* state, int64_t n_slots,
+                                         const int32_t* slots, void* o, int64_t ldo,
+                                         nvfp4_stream_t stream);
+
 /*
  * nvfp4_selftest_gemm_stall — failure-detection self-test of the GEMM
  * kernels themselves (no counterpart on the pages; it exists so that the
@@ -464,7 +546,8 @@ nvfp4_status nvfp4_selftest_gemm_stall(const uint8_t* a_codes, const uint8_t* a_
                                        nvfp4_stream_t stream);
 
 /*
- * nvfp4_read_fault — every mbarrier wait in the GEMM kernel is bounded; on
+ * nvfp4_read_fault — every mbarrier wait in the GEMM and linear-attention
+ * kernels (bits 512, 1024, 2048) is bounded; on
  * expiry the kernel records a nonzero fault word, stops issuing work and
  * returns instead of hanging. This call synchronises `stream`, copies the
  * fault word to *fault_out (0 = none) and clears it. Returns NVFP4_ERR_TIMEOUT

@@ -23,6 +23,8 @@
 #include "fold.cuh"
 #include "gemm_sm100.cuh"
 #include "gemm_skinny.cuh"
+#include "linear_attention.cuh"
+#include "linear_attention_step.cuh"
 #include "quant.cuh"
 #include "silu_mul.cuh"
 
@@ -44,6 +46,7 @@ struct DeviceState {
   int sms = 0;
   unsigned gemm_smem_set = 0;         // bit per instantiation (plain, epilogue)
   unsigned skinny_smem_set = 0;       // bit per token-tile instantiation
+  unsigned la_smem_set = 0;           // bit per linear-attention instantiation
   int amax_per_sm = 0;                // resident CTAs per SM of the quantizer's kernels
   int quant_per_sm = 0;
   float* noalloc_partials = nullptr;  // device address of g_noalloc_partials in ctx_id
@@ -1170,6 +1173,203 @@ nvfp4_status nvfp4_fuse_group_scales(int n_modules, const int64_t* rows_per_modu
   fold_kernel<<<static_cast<unsigned>(blocks), kThreads, 0,
                 reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return launch_status();
+}
+
+}  // extern "C"
+
+namespace {
+
+// Whether two [rows][..] matrices share bytes: `ca` columns of `ea` bytes at
+// pitch lda, `cb` of `eb` bytes at pitch ldb. Disjoint columns of one matrix
+// (same pitch in bytes) do not.
+bool rows_overlap(const void* a, int64_t lda, int64_t ca, int64_t ea, const void* b, int64_t ldb,
+                  int64_t cb, int64_t eb, int64_t rows) {
+  if (a == nullptr || b == nullptr || rows < 1) return false;
+  const int64_t a0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a));
+  const int64_t b0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b));
+  const int64_t a1 = a0 + ((rows - 1) * lda + ca) * ea, b1 = b0 + ((rows - 1) * ldb + cb) * eb;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (rows == 1 || lda * ea != ldb * eb) return true;
+  const int64_t ld = lda * ea;
+  const int64_t d = (((b0 - a0) % ld) + ld) % ld;  // b's column offset from a, in bytes
+  return d < ca * ea || ld - d < cb * eb;
+}
+
+bool bytes_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  return rows_overlap(a, na, na, 1, b, nb, nb, 1, 1);
+}
+
+// What both linear-attention calls ask of their heads and rows.
+nvfp4_status check_heads(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                         int64_t ldv, const float* decay, const float* beta, int64_t rows, int h_k,
+                         int h_v, int d_k, int d_v, const float* state, int64_t n_slots,
+                         const int32_t* slots, const void* o, int64_t ldo) {
+  if (rows < 0 || h_k < 1 || h_v < 1 || d_k < 1 || d_v < 1 || n_slots < 0) return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0 && (!q || !k || !v || !decay || !o)) return NVFP4_ERR_INVALID_ARG;
+  if (h_v % h_k != 0) return NVFP4_ERR_INVALID_ARG;
+  if ((d_k != 64 && d_k != 128) || d_v % 32 != 0 || rows >= (int64_t{1} << 31) ||
+      n_slots >= (int64_t{1} << 31) || h_v > 65535 || d_v > 65535)
+    return NVFP4_ERR_UNSUPPORTED;
+  const int64_t wk = static_cast<int64_t>(h_k) * d_k, wv = static_cast<int64_t>(h_v) * d_v;
+  if (ldq < wk || ldk < wk || ldv < wv || ldo < wv) return NVFP4_ERR_INVALID_ARG;
+  if (ldq % 8 != 0 || ldk % 8 != 0 || ldv % 8 != 0 || ldo % 8 != 0 || !aligned(q, 16) ||
+      !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(decay, 4) ||
+      !aligned(beta, 4) || !aligned(state, 16) || !aligned(slots, 4))
+    return NVFP4_ERR_MISALIGNED;
+  if (rows_overlap(o, ldo, wv, 2, q, ldq, wk, 2, rows) ||
+      rows_overlap(o, ldo, wv, 2, k, ldk, wk, 2, rows) ||
+      rows_overlap(o, ldo, wv, 2, v, ldv, wv, 2, rows))
+    return NVFP4_ERR_INVALID_ARG;
+  const int64_t ob = rows > 0 ? ((rows - 1) * ldo + wv) * 2 : 0;
+  if (bytes_overlap(o, ob, decay, rows * h_v * 4) || bytes_overlap(o, ob, beta, rows * h_v * 4) ||
+      bytes_overlap(o, ob, state, n_slots * wv * d_k * 4))
+    return NVFP4_ERR_INVALID_ARG;
+  return NVFP4_OK;
+}
+
+// Chunk slots of the workspace: first_slot() of linear_attention.cuh.
+int64_t chunk_slots(int64_t total, int64_t n_seq) { return total / nvfp4::la::C + n_seq; }
+
+template <typename K>
+nvfp4_status la_smem(DeviceState* st, unsigned bit, K kernel, int bytes) {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (!(st->la_smem_set & (1u << bit))) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return NVFP4_ERR_CUDA;
+    }
+    st->la_smem_set |= 1u << bit;
+  }
+  return NVFP4_OK;
+}
+
+template <int DK, int DVB>
+nvfp4_status launch_chain(DeviceState* st, unsigned bit, const nvfp4::la::Args& a, cudaStream_t s) {
+  using namespace nvfp4::la;
+  using Cfg = ChainCfg<DK, DVB>;
+  const int64_t grid = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / DVB);
+  if (grid >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
+  if (nvfp4_status e = la_smem(st, bit, chain_kernel<DK, DVB>, Cfg::SMEM)) return e;
+  return launch_pdl(chain_kernel<DK, DVB>, static_cast<unsigned>(grid), kChainThreads, Cfg::SMEM, s,
+                    1u, a);
+}
+
+template <int DK>
+nvfp4_status launch_linear_attention(DeviceState* st, const nvfp4::la::Args& a, cudaStream_t s) {
+  using namespace nvfp4::la;
+  const unsigned base = DK == 128 ? 0u : 4u;
+  const int64_t grid = chunk_slots(a.total, a.n_seq) * a.h_v;
+  if (grid >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
+  if (nvfp4_status e = la_smem(st, base, prepare_kernel<DK>, PrepCfg<DK>::SMEM)) return e;
+  if (nvfp4_status e = launch_pdl(prepare_kernel<DK>, static_cast<unsigned>(grid), kPrepThreads,
+                                  PrepCfg<DK>::SMEM, s, 1u, a))
+    return e;
+  return launch_chain<DK, 32>(st, base + 1, a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nvfp4_linear_attention_workspace_bytes(int64_t total, int64_t n_seq, int h_k, int h_v,
+                                              int d_k) {
+  if (total < 0 || n_seq < 1 || h_k < 1 || h_v < 1 || (d_k != 64 && d_k != 128)) return 0;
+  return static_cast<size_t>(chunk_slots(total, n_seq)) *
+         (static_cast<size_t>(h_k) * nvfp4::la::kq_bytes(d_k) +
+          static_cast<size_t>(h_v) * nvfp4::la::kHeadBytes);
+}
+
+nvfp4_status nvfp4_linear_attention(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                    const void* v, int64_t ldv, const float* decay,
+                                    const float* beta, float scale, int64_t total, int h_k,
+                                    int h_v, int d_k, int d_v, int64_t n_seq,
+                                    const int32_t* cu_seqlens, float* state, int64_t n_slots,
+                                    const int32_t* slots, const int32_t* resume, void* o,
+                                    int64_t ldo, void* workspace, size_t workspace_bytes,
+                                    nvfp4_stream_t stream) {
+  using namespace nvfp4::la;
+  if (nvfp4_status e = check_heads(q, ldq, k, ldk, v, ldv, decay, beta, total, h_k, h_v, d_k, d_v,
+                                   state, n_slots, slots, o, ldo))
+    return e;
+  if (n_seq < 1 || workspace == nullptr || (cu_seqlens == nullptr && n_seq != 1) ||
+      (state == nullptr && (slots != nullptr || resume != nullptr)) ||
+      (state != nullptr && slots == nullptr && n_slots < n_seq))
+    return NVFP4_ERR_INVALID_ARG;
+  if (n_seq >= (int64_t{1} << 31) || chunk_slots(total, n_seq) >= (int64_t{1} << 31))
+    return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(workspace, 256) || !aligned(cu_seqlens, 4) || !aligned(resume, 4))
+    return NVFP4_ERR_MISALIGNED;
+  if (workspace_bytes < nvfp4_linear_attention_workspace_bytes(total, n_seq, h_k, h_v, d_k))
+    return NVFP4_ERR_INVALID_ARG;
+  int dev;
+  DeviceState* st;
+  if (nvfp4_status e = current_device(&dev, &st)) return e;
+  Args a;
+  std::memset(&a, 0, sizeof a);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.ldo = ldo;
+  a.decay = decay;
+  a.beta = beta;
+  a.scale = scale;
+  a.total = static_cast<int>(total);
+  a.h_k = h_k;
+  a.h_v = h_v;
+  a.d_v = d_v;
+  a.n_seq = static_cast<int>(n_seq);
+  a.cu = cu_seqlens;
+  a.state = state;
+  a.n_slots = static_cast<int>(n_slots);
+  a.slots = slots;
+  a.resume = resume;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.kq = static_cast<uint8_t*>(workspace);
+  a.tt = a.kq + chunk_slots(total, n_seq) * h_k * kq_bytes(d_k);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return d_k == 128 ? launch_linear_attention<128>(st, a, s) : launch_linear_attention<64>(st, a, s);
+}
+
+nvfp4_status nvfp4_linear_attention_step(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                         const void* v, int64_t ldv, const float* decay,
+                                         const float* beta, float scale, int64_t batch, int h_k,
+                                         int h_v, int d_k, int d_v, float* state, int64_t n_slots,
+                                         const int32_t* slots, void* o, int64_t ldo,
+                                         nvfp4_stream_t stream) {
+  using namespace nvfp4::la;
+  if (nvfp4_status e = check_heads(q, ldq, k, ldk, v, ldv, decay, beta, batch, h_k, h_v, d_k, d_v,
+                                   state, n_slots, slots, o, ldo))
+    return e;
+  if (state == nullptr || (slots == nullptr && n_slots < batch)) return NVFP4_ERR_INVALID_ARG;
+  const int64_t grid = batch * h_v * (d_v / kStepCols);
+  if (grid >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
+  if (batch == 0) return NVFP4_OK;
+  StepArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.ldo = ldo;
+  a.decay = decay;
+  a.beta = beta;
+  a.scale = scale;
+  a.batch = static_cast<int>(batch);
+  a.h_k = h_k;
+  a.h_v = h_v;
+  a.d_v = d_v;
+  a.state = state;
+  a.n_slots = static_cast<int>(n_slots);
+  a.slots = slots;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  return launch_pdl(d_k == 128 ? step_kernel<128> : step_kernel<64>, static_cast<unsigned>(grid),
+                    kStepThreads, 0, reinterpret_cast<cudaStream_t>(stream), 1u, a);
 }
 
 nvfp4_status nvfp4_silu_mul(const void* y, int64_t m, int64_t n, int64_t ldy, void* h,

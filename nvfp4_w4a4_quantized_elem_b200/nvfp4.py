@@ -36,6 +36,8 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_sf_bytes", "nvfp4_quantize_workspace_by
            "nvfp4_gemm_swiglu_quant",
            "nvfp4_gemm_swiglu_quant_dynamic_workspace_bytes", "nvfp4_gemm_swiglu_quant_dynamic",
            "nvfp4_fuse_group_scales", "nvfp4_silu_mul", "nvfp4_read_fault",
+           "nvfp4_linear_attention_workspace_bytes", "nvfp4_linear_attention",
+           "nvfp4_linear_attention_step",
            "nvfp4_selftest_wait_timeout", "nvfp4_selftest_gemm_stall")
 
 # activations of the GEMM epilogue (nvfp4_activation)
@@ -85,6 +87,11 @@ def lib() -> ctypes.CDLL:
                                                     P, SZ, P]),
             "nvfp4_fuse_group_scales": (I, [I, P, I64, P, P, P, P, P]),
             "nvfp4_silu_mul": (I, [P, I64, I64, I64, P, I64, P]),
+            "nvfp4_linear_attention_workspace_bytes": (SZ, [I64, I64, I, I, I]),
+            "nvfp4_linear_attention": (I, [P, I64, P, I64, P, I64, P, P, ctypes.c_float, I64, I, I,
+                                           I, I, I64, P, P, I64, P, P, P, I64, P, SZ, P]),
+            "nvfp4_linear_attention_step": (I, [P, I64, P, I64, P, I64, P, P, ctypes.c_float, I64,
+                                                I, I, I, I, P, I64, P, P, I64, P]),
             "nvfp4_read_fault": (I, [P, U32P]),
             "nvfp4_selftest_wait_timeout": (I, [ctypes.c_uint64, P]),
             "nvfp4_selftest_gemm_stall": (I, [P, P, P, P, P, P, P, I64, I64, I64, ctypes.c_uint64,
@@ -374,6 +381,105 @@ def silu_mul(y: torch.Tensor, out: torch.Tensor | None = None,
     st = lib().nvfp4_silu_mul(_ptr(y), m, n, y.stride(0), _ptr(out), out.stride(0),
                               _stream(stream))
     _check(st, "nvfp4_silu_mul")
+    return out
+
+
+def _heads(q, k, v, decay, beta, state, out):
+    """Checked arguments shared by linear_attention and its step: (h_k, h_v,
+    d_k, d_v, row pitches of q, k, v and out, out)."""
+    for t, name, dt in ((q, "q", torch.bfloat16), (k, "k", torch.bfloat16),
+                        (v, "v", torch.bfloat16), (decay, "decay", torch.float32),
+                        (beta, "beta", torch.float32), (state, "state", torch.float32),
+                        (out, "out", torch.bfloat16)):
+        if t is not None:
+            _require_cuda(t, name, dt)
+            if t.device != q.device:
+                raise ValueError(f"{name} must be on {q.device}")
+    if q.device.index != torch.cuda.current_device():
+        raise ValueError(f"q is on {q.device}, the current device is {torch.cuda.current_device()}")
+    if q.dim() != 3 or v.dim() != 3 or q.shape != k.shape or v.shape[0] != q.shape[0]:
+        raise ValueError("q and k must be [rows, h_k, d_k], v [rows, h_v, d_v]")
+    rows, hk, dk = q.shape
+    _, hv, dv = v.shape
+    for t, name in ((decay, "decay"), (beta, "beta")):
+        if t is not None and (tuple(t.shape) != (rows, hv) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous [{rows}, {hv}]")
+    if state is not None and (state.dim() != 4 or tuple(state.shape[1:]) != (hv, dk, dv)
+                              or not state.is_contiguous()):
+        raise ValueError(f"state must be contiguous [slots, {hv}, {dk}, {dv}]")
+    if out is None:
+        out = torch.empty((rows, hv, dv), dtype=torch.bfloat16, device=q.device)
+    elif tuple(out.shape) != (rows, hv, dv):
+        raise ValueError(f"out must be [{rows}, {hv}, {dv}]")
+    pitches = []
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+        h, d = t.shape[1], t.shape[2]
+        if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+            raise ValueError(f"the heads of a row of {name} must be contiguous")
+        pitches.append(t.stride(0) if rows > 1 else -(-h * d // 8) * 8)
+    return hk, hv, dk, dv, pitches, out
+
+
+def _int32(t: torch.Tensor | None, name: str, n: int, device) -> None:
+    if t is not None:
+        _require_cuda(t, name, torch.int32)
+        if tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be a contiguous vector of {n} on {device}")
+
+
+def linear_attention_workspace_bytes(total: int, n_seq: int, h_k: int, h_v: int, d_k: int) -> int:
+    return int(lib().nvfp4_linear_attention_workspace_bytes(total, n_seq, h_k, h_v, d_k))
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
+                     beta: torch.Tensor | None = None, *, cu_seqlens: torch.Tensor | None = None,
+                     state: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                     resume: torch.Tensor | None = None, scale: float | None = None,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """nvfp4_linear_attention: gated linear attention over packed prompts; with
+    ``beta`` the gated delta rule. q, k bf16 [total, h_k, d_k], v bf16 [total,
+    h_v, d_v] (views of a fused projection are fine), decay (log) and beta FP32
+    [total, h_v]; ``cu_seqlens`` int32 [n_seq + 1] (None: one sequence); final
+    states go to ``state`` FP32 [slots, h_v, d_k, d_v] at ``slots`` (int32
+    [n_seq], None: in order), and come from there where ``resume`` (int32
+    [n_seq]) is nonzero. ``scale`` defaults to d_k ** -0.5. The workspace is
+    allocated on ``stream`` when None."""
+    hk, hv, dk, dv, (ldq, ldk, ldv, ldo), out = _heads(q, k, v, decay, beta, state, out)
+    total = q.shape[0]
+    n_seq = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    _int32(cu_seqlens, "cu_seqlens", n_seq + 1, q.device)
+    _int32(slots, "slots", n_seq, q.device)
+    _int32(resume, "resume", n_seq, q.device)
+    if workspace is None:
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(linear_attention_workspace_bytes(total, n_seq, hk, hv, dk),
+                                    dtype=torch.uint8, device=q.device)
+    st = lib().nvfp4_linear_attention(
+        _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(decay), _ptr(beta),
+        dk ** -0.5 if scale is None else scale, total, hk, hv, dk, dv, n_seq, _ptr(cu_seqlens),
+        _ptr(state), 0 if state is None else state.shape[0], _ptr(slots), _ptr(resume), _ptr(out),
+        ldo, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "nvfp4_linear_attention")
+    return out
+
+
+def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
+                          beta: torch.Tensor | None = None, *, state: torch.Tensor,
+                          slots: torch.Tensor | None = None, scale: float | None = None,
+                          out: torch.Tensor | None = None,
+                          stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """nvfp4_linear_attention_step: one token per row, states updated in place.
+    Shapes as linear_attention with rows = batch; ``slots`` int32 [batch] (None:
+    row i uses slot i), a slot outside the pool marks a padding row."""
+    hk, hv, dk, dv, (ldq, ldk, ldv, ldo), out = _heads(q, k, v, decay, beta, state, out)
+    batch = q.shape[0]
+    _int32(slots, "slots", batch, q.device)
+    st = lib().nvfp4_linear_attention_step(
+        _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(decay), _ptr(beta),
+        dk ** -0.5 if scale is None else scale, batch, hk, hv, dk, dv, _ptr(state),
+        state.shape[0], _ptr(slots), _ptr(out), ldo, _stream(stream))
+    _check(st, "nvfp4_linear_attention_step")
     return out
 
 

@@ -9,14 +9,15 @@
 // DeltaNet form its text describes.)
 // Over a chunk with start state S, G_t = g_1 + .. + g_t, and rows of K, Q, V, U
 // per token, unrolling gives
-//   (I + L) U = diag(beta) (V - diag(e^G) K S),  L_tj = beta_t e^{G_t-G_j} k_t.k_j, j < t
-//   O = diag(e^G) Q S + A U,                      A_tj = e^{G_t-G_j} q_t.k_j, j <= t
-//   S' = e^{G_64} S + K^T diag(e^{G_64-G}) U
-// so with T = (I + L)^-1 diag(beta) and X = V - diag(e^G) K S
-//   [U; O - diag(e^G) Q S] = [T; A T] X:
-// three products per chunk depend on one another, [K; Q] S, [T; AT] X and
-// K^T U~, all with 128 rows on the MMA's M side (tokens of K and Q together,
-// then of U and O together, then d_k) and a block of d_v columns as its N.
+//   (I + L) U = X,  X = diag(beta) (V - diag(e^G) K S)
+//     L_tj = beta_t e^{G_t-G_j} k_t.k_j for j < t
+//   O = diag(e^G) Q S + A U,  A_tj = e^{G_t-G_j} q_t.k_j for j <= t
+//   S' = e^{G_64} S + K^T U~,  U~ = diag(e^{G_64-G}) U
+// so with T = (I + L)^-1:  [U; O - diag(e^G) Q S] = [T; A T] X. Three products
+// per chunk depend on one another, [K; Q] S, [T; AT] X and K^T U~, all with
+// 128 rows on the MMA's M side (tokens of K and Q together, then of U and O
+// together, then d_k) and a block of d_v columns as its N. Without the delta
+// rule T = I and X = V.
 //
 // Two kernels. prepare_kernel, parallel over chunks and heads, computes what
 // does not depend on S: the swizzled bf16 image of [K; Q] (rows past a
@@ -24,19 +25,19 @@
 // sequence's chunks in order, one CTA per (sequence, head, d_v block), with S
 // in FP32 registers.
 //
-// Precision: q, k, v are bf16 and enter the products exactly. S, X, U, T, A
-// are FP32 values; as MMA operands each is split into bf16 hi + lo (16 bits,
-// residual 2^-17 of the value), products hi hi + hi lo + lo hi, accumulated
-// in FP32: one bf16 operand alone would leave 2^-9 in the FP32 states. G is
-// summed in FP64: the difference of two FP32 sums of strong decays would lose
-// the weak decays between them.
+// Precision: q, k, v are bf16 and enter the products exactly. The FP32 operands
+// S, X and U~ are cut into three bf16 pieces (24 bits, nothing is lost), T and
+// A T into two (2^-17 of them is lost, but T's unit diagonal, beta standing in
+// X, is exact); products are accumulated in FP32. One bf16 operand alone would
+// leave 2^-9 in the FP32 states. G is summed in FP64 and kept as two FP32
+// parts: the difference of two FP32 sums of strong decays would lose the weak
+// decays between them.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cstdint>
 
 #include "fault.cuh"
-#include "gemm_skinny.cuh"
 #include "ptx.cuh"
 
 namespace nvfp4 {
@@ -45,9 +46,10 @@ namespace la {
 constexpr int C = 64;                       // tokens per chunk
 constexpr int kHalfBytes = 128 * 128;       // [K; Q] image: 128 rows x 64 of d_k
 constexpr int kTTBytes = 128 * 128;         // [T; AT] image: 128 rows x 64, one piece
-constexpr int kGateFloats = 2 * C + 4;      // e^G, e^{G_64 - G}, e^{G_64}
+constexpr int kGateFloats = 3 * C + 4;      // e^G, e^{G_64 - G}, beta, e^{G_64}
 constexpr int kGateBytes = (kGateFloats * 4 + 127) / 128 * 128;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 100000000ull;
 
 enum : uint32_t { kFaultPrepare = 512u, kFaultChainMma = 1024u, kFaultChain = 2048u };
 
@@ -90,12 +92,20 @@ __device__ __forceinline__ void seq_range(const Args& a, int b, int& start, int&
 // below total/64 + n_seq.
 __device__ __forceinline__ int first_slot(int start, int b) { return start / C + b; }
 
-// Two FP32 values -> packed bf16 hi parts, and the packed bf16 of the rests.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+// An FP32 value is the sum of three bf16 values, its 24 bits cut 8 by 8: the
+// upper half-word of x, of the (exact) rest, and of the rest of that. Takes the
+// next piece of x and y, packed, and leaves the rests in them.
+__device__ __forceinline__ uint32_t take_piece(float& x, float& y) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  x -= __uint_as_float(a & 0xFFFF0000u);
+  y -= __uint_as_float(b & 0xFFFF0000u);
+  return __byte_perm(a, b, 0x7632);
+}
+
+// The last of two pieces is rounded instead: 2^-17 of the value is left.
+__device__ __forceinline__ uint32_t round_piece(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(x - __low2float(h), y - __high2float(h));
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Row `k` of an MN-major operand without swizzle (8 x 16-byte core matrices,
@@ -104,24 +114,49 @@ __device__ __forceinline__ uint32_t mn_off(int k, int n8, int n_stride) {
   return static_cast<uint32_t>((k >> 3) * 128 + (k & 7) * 16 + n8 * n_stride);
 }
 
-// N FP32 values of operand row k -> hi and lo pieces in shared memory.
-template <int N>
-__device__ __forceinline__ void store_row_split(uint32_t hi_base, uint32_t lo_base, int k,
-                                                int n_stride, const float (&x)[N]) {
+// N FP32 values of operand row k -> PIECES bf16 pieces, `piece` bytes apart.
+template <int PIECES, int N>
+__device__ __forceinline__ void store_row_split(uint32_t base, int piece, int k, int n_stride,
+                                                const float (&x)[N]) {
 #pragma unroll
   for (int n8 = 0; n8 < N / 8; ++n8) {
-    uint32_t h[4], l[4];
+    float r[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split2(x[8 * n8 + 2 * e], x[8 * n8 + 2 * e + 1], h[e], l[e]);
-    const uint32_t off = mn_off(k, n8, n_stride);
-    ptx::st_shared_v4(hi_base + off, h[0], h[1], h[2], h[3]);
-    ptx::st_shared_v4(lo_base + off, l[0], l[1], l[2], l[3]);
+    for (int e = 0; e < 8; ++e) r[e] = x[8 * n8 + e];
+    const uint32_t at = base + mn_off(k, n8, n_stride);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = PIECES == 2 && p == 1 ? round_piece(r[2 * e], r[2 * e + 1])
+                                     : take_piece(r[2 * e], r[2 * e + 1]);
+      ptx::st_shared_v4(at + p * piece, w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
 // 16-byte unit `u` of row r in a 128-byte-row, 128-byte-swizzled image.
 __device__ __forceinline__ uint32_t sw128(int r, int u) {
   return static_cast<uint32_t>(r * 128 + ((u ^ (r & 7)) << 4));
+}
+
+// 64 FP32 values of row r -> hi and lo images of the rows (`piece` apart).
+__device__ __forceinline__ void store_image_row(uint32_t base, int piece, int r, const float* x) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = x[8 * u + e];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = p == 1 ? round_piece(v[2 * e], v[2 * e + 1]) : take_piece(v[2 * e], v[2 * e + 1]);
+      ptx::st_shared_v4(base + p * piece + sw128(r, u), w[0], w[1], w[2], w[3]);
+    }
+  }
 }
 
 template <int N>
@@ -137,70 +172,187 @@ __device__ __forceinline__ void tc_ld(uint32_t taddr, float (&x)[N]) {
   ptx::tc_wait_ld();
 }
 
+// Bounded wait (2 s): many tries between two looks at the clock, since the
+// waits of the chain are short and stand one behind the other.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
+                                             volatile uint32_t* abort_flag, uint32_t who) {
+  for (int i = 0; i < 64; ++i)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1u;
+      atomicOr(&g_fault_word, who);
+      return false;
+    }
+  }
+}
+
+// Used only while aborting: wait for in-flight asynchronous work, bounded.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (ptx::globaltimer_ns() - t0 > kDrainLimitNs) return;
+  }
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
                                           volatile uint32_t* abort_flag, uint32_t who) {
-  return __all_sync(0xFFFFFFFFu,
-                    skinny::wait_bounded(bar, parity, abort_flag, who, kWaitLimitNs));
+  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, who));
 }
 
 // ------------------------------------------------------------------ prepare --
 
 constexpr int kPrepThreads = 128;
-constexpr int kLd = 65;                       // row pitch of the FP32 64x64 tiles
-constexpr int kTileBytes = (C * kLd * 4 + 127) / 128 * 128;
+constexpr int kLd = 68;                       // row pitch (floats) of the 64x64 tiles
+constexpr int kTileBytes = C * kLd * 4;
+constexpr int kMLd = 20;                      // row pitch of the inverse's 16x16 scratch
+constexpr int kMBytes = 16 * kMLd * 4;
 
+// Shared memory: the [K; Q] image, over which L and T = (I + L)^-1 are written
+// once the scores are taken; T's pieces go over L, the two pieces of the
+// [T; AT] image over T and, the product A T done, over T's pieces. A's pieces
+// are the rows 64..127 of 128-row operands whose rows 0..63 lie in whatever
+// stands before them: those rows of the product are not read.
 template <int DK>
 struct PrepCfg {
   static constexpr int KQ = kq_bytes(DK);
-  static constexpr int A_OFF = KQ;                       // A pieces, then the image (2 x 16 KiB)
-  static constexpr int L_OFF = A_OFF + 2 * kTTBytes;     // L (FP32), then T's pieces
-  static constexpr int T_OFF = L_OFF + kTileBytes;       // (I + L)^-1 (FP32)
-  static constexpr int M_OFF = T_OFF + kTileBytes;       // 32x33 scratch of the inverse
-  static constexpr int G_OFF = M_OFF + 32 * 33 * 4 + 128;
-  static constexpr int SMEM = 1024 + G_OFF + C * 8 + C * 4 + 64;
+  static constexpr int L_OFF = 0;
+  static constexpr int T_OFF = kTileBytes;
+  static constexpr int A_OFF = 2 * kTileBytes;             // hi rows, then lo rows
+  static constexpr int A_PIECE = kTTBytes / 2;
+  static constexpr int G_OFF = A_OFF + 2 * A_PIECE;        // G, beta
+  static constexpr int M_OFF = G_OFF + C * 8 + C * 4;      // scratch of the inverse
+  static constexpr int BAR_OFF = M_OFF + 3 * kMBytes;
+  static constexpr int SMEM = 1024 + BAR_OFF + 64;
+  static_assert(KQ <= A_OFF && kTTBytes <= kTileBytes && kTileBytes % 1024 == 0, "regions");
 };
 
-// (I + L)^-1 of the strictly lower triangular L (FP32, unit diagonal implied):
-// the four 16x16 diagonal blocks by forward substitution, one thread per
-// column; then twice [P 0; L21 Q]^-1 = [P^-1 0; -Q^-1 L21 P^-1 Q^-1].
+// acc[i][4] (+)= rows r0 + 8 i of A times B, 16 x 16 blocks of pitch lda, ldb;
+// this thread's columns c4 .. c4 + 3.
+template <int NR>
+__device__ __forceinline__ void block_mac(float (&acc)[NR][4], const float* A, int lda,
+                                          const float* B, int ldb, int r0, int c4) {
+#pragma unroll
+  for (int m = 0; m < 16; m += 4) {
+    float4 a[NR], b[4];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) a[i] = *reinterpret_cast<const float4*>(A + (r0 + 8 * i) * lda + m);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (m + j) * ldb + c4);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const float av[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][0] += av[j] * b[j].x;
+        acc[i][1] += av[j] * b[j].y;
+        acc[i][2] += av[j] * b[j].z;
+        acc[i][3] += av[j] * b[j].w;
+      }
+    }
+  }
+}
+
+// Blocks of T = (I + L)^-1 D block diagonals below the main one: T_ij =
+// -T_ii sum_{j <= m < i} L_im T_mj for i = j + D, WPB warps per block (16/WPB
+// rows each). M: one 16x16 scratch per block.
+template <int D, int WPB>
+__device__ __forceinline__ void invert_diagonal(const float* L, float* T, float* M, int t) {
+  constexpr int NB = 4 - D, RW = 16 / WPB, NR = RW >= 16 ? 2 : 1;
+  const int warp = t >> 5, lane = t & 31;
+  const int blk = warp / WPB, j = blk, i = j + D;
+  const int c4 = (lane & 3) * 4, r0 = (warp % WPB) * RW + (lane >> 2);
+  const bool on = blk < NB && (lane >> 2) < RW;
+  float* const m = M + blk * 16 * kMLd;
+  float acc[NR][4];
+  auto clear = [&] {
+#pragma unroll
+    for (int a = 0; a < NR; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[a][b] = 0.0f;
+  };
+  if (on) {
+    clear();
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+      block_mac<NR>(acc, L + 16 * i * kLd + 16 * (j + k), kLd, T + 16 * (j + k) * kLd + 16 * j, kLd, r0, c4);
+#pragma unroll
+    for (int a = 0; a < NR; ++a)
+      *reinterpret_cast<float4*>(m + (r0 + 8 * a) * kMLd + c4) =
+          make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
+  }
+  __syncthreads();
+  if (on) {
+    clear();
+    block_mac<NR>(acc, T + 16 * i * kLd + 16 * i, kLd, m, kMLd, r0, c4);
+#pragma unroll
+    for (int a = 0; a < NR; ++a)
+      *reinterpret_cast<float4*>(T + (16 * i + r0 + 8 * a) * kLd + 16 * j + c4) =
+          make_float4(-acc[a][0], -acc[a][1], -acc[a][2], -acc[a][3]);
+  }
+  __syncthreads();
+}
+
+// T = (I + L)^-1 for the strictly lower triangular L, in FP32 by 16x16 blocks:
+// the diagonal ones by forward substitution, one thread per column, then one
+// block diagonal after the other. 87 K multiply-adds per chunk and head, on
+// the FP32 units: as split bf16 products the 16-wide blocks would spend more on
+// splitting and moving operands than on arithmetic.
 __device__ __forceinline__ void invert_unit_lower(const float* L, float* T, float* M, int t) {
   if (t < C) {
     const int b0 = t & ~15, j = t & 15;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float s = i == j ? 1.0f : 0.0f;
+      float s[4] = {i == j ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int m = 0; m < i; ++m) s -= L[(b0 + i) * kLd + b0 + m] * x[m];
-      x[i] = i < j ? 0.0f : s;
+      for (int m = 0; m < i; m += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(L + (b0 + i) * kLd + b0 + m);
+        s[0] -= l.x * x[m];  // L is zero from the diagonal on
+        if (m + 1 < i) s[1] -= l.y * x[m + 1];
+        if (m + 2 < i) s[2] -= l.z * x[m + 2];
+        if (m + 3 < i) s[3] -= l.w * x[m + 3];
+      }
+      x[i] = i < j ? 0.0f : (s[0] + s[1]) + (s[2] + s[3]);
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) T[(b0 + i) * kLd + b0 + j] = x[i];
   }
   __syncthreads();
-#pragma unroll 1
-  for (int w = 16; w < C; w *= 2) {
-    const int per = w * w, n = per * (C / (2 * w));
-    for (int i = t; i < n; i += kPrepThreads) {   // M = L21 P^-1
-      const int b = i / per, r = (i % per) / w, c = i % w, o = 2 * w * b;
-      float s = 0.0f;
-      for (int m = c; m < w; ++m) s += L[(o + w + r) * kLd + o + m] * T[(o + m) * kLd + o + c];
-      M[b * w * 17 * (w / 16) + r * (w + 1) + c] = s;
-    }
-    __syncthreads();
-    for (int i = t; i < n; i += kPrepThreads) {   // T21 = -Q^-1 M
-      const int b = i / per, r = (i % per) / w, c = i % w, o = 2 * w * b;
-      float s = 0.0f;
-      for (int m = 0; m <= r; ++m)
-        s += T[(o + w + r) * kLd + o + w + m] * M[b * w * 17 * (w / 16) + m * (w + 1) + c];
-      T[(o + w + r) * kLd + o + c] = -s;
-    }
-    __syncthreads();
+  invert_diagonal<1, 1>(L, T, M, t);
+  invert_diagonal<2, 2>(L, T, M, t);
+  invert_diagonal<3, 4>(L, T, M, t);
+}
+
+// 2^x, zero below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// x[j] *= f e^{G_t - G_j} for j <= last, zero beyond (a score that is not
+// finite, too). Without branches: a branch per block of columns puts x into
+// local memory.
+__device__ __forceinline__ void decay_row(float (&x)[C], const float2* G, int row, int last,
+                                          float f) {
+  const float2 gt = G[row];
+#pragma unroll
+  for (int j = 0; j < C; j += 2) {
+    const float4 g = *reinterpret_cast<const float4*>(G + j);
+    const float e0 = f * ex2((gt.x - g.x) + (gt.y - g.y));
+    const float e1 = f * ex2((gt.x - g.z) + (gt.y - g.w));
+    x[j] = j <= last ? e0 * x[j] : 0.0f;
+    x[j + 1] = j + 1 <= last ? e1 * x[j + 1] : 0.0f;
   }
 }
 
 template <int DK>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 4)
     prepare_kernel(const Args a) {
   using P = PrepCfg<DK>;
   extern __shared__ uint8_t smem_raw[];
@@ -209,29 +361,15 @@ __global__ void __launch_bounds__(kPrepThreads)
   float* const L = reinterpret_cast<float*>(smem + P::L_OFF);
   float* const T = reinterpret_cast<float*>(smem + P::T_OFF);
   float* const M = reinterpret_cast<float*>(smem + P::M_OFF);
-  double* const G = reinterpret_cast<double*>(smem + P::G_OFF);
+  float2* const G = reinterpret_cast<float2*>(smem + P::G_OFF);  // G log2(e), two parts
   float* const Beta = reinterpret_cast<float*>(G + C);
-  uint64_t* const bar = reinterpret_cast<uint64_t*>(Beta + C);
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bar + 1);
   volatile uint32_t* const abort_flag = tmem_holder + 1;
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int h = blockIdx.x % a.h_v, hk = h / (a.h_v / a.h_k);
+  const int h = blockIdx.x % a.h_v, group = a.h_v / a.h_k, hk = h / group;
   const int slot = blockIdx.x / a.h_v;
-  ptx::grid_dep_launch();
-  ptx::grid_dep_wait();
-  // the last sequence whose first slot is at or below this one
-  int lo = 0, hi = a.n_seq - 1, start, end;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    seq_range(a, mid, start, end);
-    if (first_slot(start, mid) <= slot) lo = mid; else hi = mid - 1;
-  }
-  seq_range(a, lo, start, end);
-  const int64_t tok0 = start + static_cast<int64_t>(slot - first_slot(start, lo)) * C;
-  if (slot < first_slot(start, lo) || tok0 >= end) return;
-  const int len = static_cast<int>(min(static_cast<int64_t>(C), end - tok0));
-
   if (t == 0) {
     ptx::mbar_init(bar, 1);
     *abort_flag = 0u;
@@ -241,35 +379,84 @@ __global__ void __launch_bounds__(kPrepThreads)
     ptx::tmem_alloc(tmem_holder, 128);
     ptx::tmem_relinquish();
   }
-  // [K; Q] -> the swizzled image, rows past the sequence zero
-  constexpr int kUnits = DK / 8;
-  for (int i = t; i < 128 * kUnits; i += kPrepThreads) {
-    const int r = i / kUnits, u = i % kUnits, tok = r & (C - 1);
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (tok < len) {
-      const __nv_bfloat16* row = r < C ? a.k + (tok0 + tok) * a.ldk : a.q + (tok0 + tok) * a.ldq;
-      x = *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(hk) * DK + 8 * u);
+  ptx::grid_dep_launch();
+  ptx::grid_dep_wait();
+  // the last sequence whose first slot is at or below this one: the slots of
+  // later sequences are higher, so it is the count of those, less one
+  int seq = -1, start = 0, end = 0;
+  for (int i = 0; i < a.n_seq; i += kPrepThreads) {
+    bool below = false;
+    if (i + t < a.n_seq) {
+      seq_range(a, i + t, start, end);
+      below = first_slot(start, i + t) <= slot;
     }
-    *reinterpret_cast<uint4*>(smem + (u / 8) * kHalfBytes + sw128(r, u % 8)) = x;
+    const int n = __syncthreads_count(below);
+    seq += n;
+    if (n < kPrepThreads) break;
   }
-  // G_t in FP64 (a decay of e^-1000 is zero in FP32 and FP64 sums keep the
-  // weak ones beside it, so -inf counts as that), beta
+  if (seq >= 0) seq_range(a, seq, start, end);
+  const int64_t tok0 = start + static_cast<int64_t>(slot - first_slot(start, seq)) * C;
+  const int len = seq < 0 || tok0 < start || tok0 >= end
+                      ? 0 : static_cast<int>(min(static_cast<int64_t>(C), end - tok0));
+  if (len == 0) {  // a slot between two sequences' chunks
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc(*tmem_holder, 128);
+    return;
+  }
+
+  // decays and beta, requested before the keys, whose loads cover them
+  double x0 = 0.0, x1 = 0.0;
+  float bt = 0.0f;
   if (warp == 0) {
-    const int i0 = 2 * lane;
     const float* g = a.decay + tok0 * a.h_v + h;
-    const double x0 = i0 < len ? fmax(static_cast<double>(g[static_cast<int64_t>(i0) * a.h_v]), -1000.0) : 0.0;
-    const double x1 = i0 + 1 < len ? fmax(static_cast<double>(g[static_cast<int64_t>(i0 + 1) * a.h_v]), -1000.0) : 0.0;
+    if (2 * lane < len) x0 = g[static_cast<int64_t>(2 * lane) * a.h_v];
+    if (2 * lane + 1 < len) x1 = g[static_cast<int64_t>(2 * lane + 1) * a.h_v];
+  } else if (warp >= 2 && t - 64 < len) {
+    bt = a.beta != nullptr ? a.beta[(tok0 + t - 64) * a.h_v + h] : 1.0f;
+  }
+  // [K; Q] -> the swizzled image, rows past the sequence zero; the group's
+  // first head also writes it out
+  {
+    constexpr int kUnits = DK / 8;  // 16-byte units per row, and per thread
+    uint8_t* const image = a.kq + (static_cast<int64_t>(slot) * a.h_k + hk) * P::KQ;
+    const int u = t % kUnits;
+    uint4 x[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int r = t / kUnits + i * (kPrepThreads / kUnits), tok = r & (C - 1);
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (tok < len) {
+        const __nv_bfloat16* row = r < C ? a.k + (tok0 + tok) * a.ldk : a.q + (tok0 + tok) * a.ldq;
+        x[i] = *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(hk) * DK + 8 * u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int r = t / kUnits + i * (kPrepThreads / kUnits);
+      const uint32_t off = (u / 8) * kHalfBytes + sw128(r, u % 8);
+      *reinterpret_cast<uint4*>(smem + off) = x[i];
+      if (h % group == 0) *reinterpret_cast<uint4*>(image + off) = x[i];
+    }
+  }
+  if (warp == 0) {
+    // G in FP64 (a decay of e^-1000 is zero, so -inf counts as that)
+    constexpr double kLog2e = 1.4426950408889634;
+    x0 = (x0 < -1000.0 ? -1000.0 : x0) * kLog2e;
+    x1 = (x1 < -1000.0 ? -1000.0 : x1) * kLog2e;
     double s = x0 + x1;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const double y = __shfl_up_sync(0xFFFFFFFFu, s, d);
       if (lane >= d) s += y;
     }
-    G[i0] = s - x1;
-    G[i0 + 1] = s;
+    const double s0 = s - x1;
+    const float h0 = static_cast<float>(s0), h1 = static_cast<float>(s);
+    G[2 * lane] = make_float2(h0, static_cast<float>(s0 - h0));
+    G[2 * lane + 1] = make_float2(h1, static_cast<float>(s - h1));
   } else if (warp >= 2) {
-    const int i = t - 64;
-    Beta[i] = i < len ? (a.beta != nullptr ? a.beta[(tok0 + i) * a.h_v + h] : 1.0f) : 0.0f;
+    Beta[t - 64] = bt;
   }
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
@@ -286,103 +473,96 @@ __global__ void __launch_bounds__(kPrepThreads)
       ptx::tc_mma_bf16(tmem, d, d, kScores, s != 0);
     }
     ptx::tc_commit(bar);
-    if (h % (a.h_v / a.h_k) == 0) {  // the group's first head writes the image
-      ptx::bulk_store(a.kq + (static_cast<int64_t>(slot) * a.h_k + hk) * P::KQ, smem, P::KQ);
-      ptx::bulk_commit_group();
-    }
   }
   bool ok = warp_wait(bar, 0, abort_flag, kFaultPrepare);
   ptx::tc_fence_after();
+  __syncthreads();  // every warp saw the scores: L may go over their operands
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
   const int row = t & (C - 1);
+  const bool delta = a.beta != nullptr;
   uint8_t* const out = a.tt + (static_cast<int64_t>(slot) * a.h_v + h) * kHeadBytes;
-  {
-    float x[C];
-    tc_ld(tmem + (static_cast<uint32_t>(warp * 32) << 16), x);
-    const double gt = G[row];
-    if (t < C) {
-      const float bt = Beta[row];
+  float x[C];
+  tc_ld(lanes, x);
+  if (t < C) {
+    const float2 gt = G[row], ge = G[C - 1];
+    const float f = Beta[row];
+    float* gate = reinterpret_cast<float*>(out + 2 * kTTBytes);
+    gate[row] = ex2(gt.x + gt.y);
+    gate[C + row] = ex2((ge.x - gt.x) + (ge.y - gt.y));
+    gate[2 * C + row] = f;
+    if (row == 0) gate[3 * C] = ex2(ge.x + ge.y);
+    if (delta) {
+      decay_row(x, G, row, row - 1, f);
 #pragma unroll
-      for (int j = 0; j < C; ++j)
-        L[row * kLd + j] = j < row ? bt * expf(static_cast<float>(gt - G[j])) * x[j] : 0.0f;
-      float* gate = reinterpret_cast<float*>(out + 2 * kTTBytes);
-      gate[row] = expf(static_cast<float>(gt));
-      gate[C + row] = expf(static_cast<float>(G[C - 1] - gt));
-      if (row == 0) gate[2 * C] = expf(static_cast<float>(G[C - 1]));
-    } else {
-      // A, zero above the diagonal, as the rows 64..127 of a K-major operand
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        uint32_t hh[4], ll[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 8 * u + 2 * e;
-          const float a0 = j <= row ? expf(static_cast<float>(gt - G[j])) * x[j] : 0.0f;
-          const float a1 = j + 1 <= row ? expf(static_cast<float>(gt - G[j + 1])) * x[j + 1] : 0.0f;
-          split2(a0, a1, hh[e], ll[e]);
-        }
-        ptx::st_shared_v4(sb + P::A_OFF + sw128(C + row, u), hh[0], hh[1], hh[2], hh[3]);
-        ptx::st_shared_v4(sb + P::A_OFF + kTTBytes + sw128(C + row, u), ll[0], ll[1], ll[2], ll[3]);
+      for (int j = 0; j < C; j += 4) {
+        *reinterpret_cast<float4*>(L + row * kLd + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        if (j >= (row & ~15) + 16)
+          *reinterpret_cast<float4*>(T + row * kLd + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
+    } else {
+      // without the delta rule T = I, and A itself stands in the place of AT
+#pragma unroll
+      for (int j = 0; j < C; ++j) x[j] = j == row ? 1.0f : 0.0f;
     }
+  } else {
+    decay_row(x, G, row, row, 1.0f);
+    if (delta) store_image_row(sb + P::A_OFF, P::A_PIECE, row, x);  // 64 rows from a multiple of 8
   }
-  if (a.beta != nullptr) {
-    for (int i = t; i < C * kLd; i += kPrepThreads) T[i] = 0.0f;
+  if (delta) {
     __syncthreads();
     invert_unit_lower(L, T, M, t);
-    float x[C];
     if (t < C) {
 #pragma unroll
-      for (int j = 0; j < C; ++j) x[j] = T[row * kLd + j] * Beta[j];
+      for (int j = 0; j < C; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(T + row * kLd + j);
+        x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
+      }
       // over L, which the inverse no longer needs
-      store_row_split(sb + P::L_OFF, sb + P::L_OFF + 8192, row, 1024, x);
+      store_row_split<2>(sb + P::L_OFF, 8192, row, 1024, x);
     }
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     if (t == 0 && ok) {
-      constexpr uint32_t kAT = ptx::idesc_bf16(128, C, false, true);
-      const uint32_t ap[3] = {0, 0, kTTBytes}, tp[3] = {0, 8192, 0};
+      // A T as A_hi [T_hi | T_lo] + A_lo T_hi over the scores, the two column
+      // blocks added by the reader
+      constexpr uint32_t kBoth = ptx::idesc_bf16(128, 2 * C, false, true);
+      constexpr uint32_t kOne = ptx::idesc_bf16(128, C, false, true);
 #pragma unroll
-      for (int c = 0; c < 3; ++c)
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int s = 0; s < C / 16; ++s)
-          ptx::tc_mma_bf16(tmem + C, ptx::smem_desc(sb + P::A_OFF + ap[c] + s * 32, 16, 1024, 2),
-                           ptx::smem_desc(sb + P::L_OFF + tp[c] + s * 256, 128, 1024, 0), kAT,
-                           (c | s) != 0);
+          ptx::tc_mma_bf16(tmem,
+                           ptx::smem_desc(sb + P::A_OFF + (p - 1) * P::A_PIECE + s * 32, 16, 1024, 2),
+                           ptx::smem_desc(sb + P::L_OFF + s * 256, 128, 1024, 0),
+                           p == 0 ? kBoth : kOne, (p | s) != 0);
       ptx::tc_commit(bar);
     }
     ok = ok && warp_wait(bar, 1, abort_flag, kFaultPrepare);
     ptx::tc_fence_after();
-    if (t >= C) tc_ld(tmem + (static_cast<uint32_t>(warp * 32) << 16) + C, x);
-    __syncthreads();  // every warp saw the product done: its operands may be overwritten
+    if (t >= C) {
+      float y[32];
+      tc_ld(lanes, x);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      uint32_t hh[4], ll[4];
+      for (int c = 0; c < C; c += 32) {
+        tc_ld(lanes + C + c, y);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split2(x[8 * u + 2 * e], x[8 * u + 2 * e + 1], hh[e], ll[e]);
-      ptx::st_shared_v4(sb + P::A_OFF + sw128(t, u), hh[0], hh[1], hh[2], hh[3]);
-      ptx::st_shared_v4(sb + P::A_OFF + kTTBytes + sw128(t, u), ll[0], ll[1], ll[2], ll[3]);
+        for (int j = 0; j < 32; ++j) x[c + j] += y[j];
+      }
     }
-  } else if (t < C) {
-    // without the delta rule T = I (exact in its hi piece) and AT = A stands
-    // in its rows already
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const uint32_t one = (row >> 3) == u ? 0x3F80u << (16 * (row & 1)) : 0u;
-      const int e = (row & 7) >> 1;
-      ptx::st_shared_v4(sb + P::A_OFF + sw128(row, u), e == 0 ? one : 0u, e == 1 ? one : 0u,
-                        e == 2 ? one : 0u, e == 3 ? one : 0u);
-      ptx::st_shared_v4(sb + P::A_OFF + kTTBytes + sw128(row, u), 0u, 0u, 0u, 0u);
-    }
+    __syncthreads();  // every warp saw the product done: the image may go over T's pieces
   }
+  // hi image at T_OFF, lo image at L_OFF
+  store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, t, x);
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();
   if (t == 0) {
-    ptx::bulk_store(out, smem + P::A_OFF, 2 * kTTBytes);
+    ptx::bulk_store(out, smem + P::T_OFF, kTTBytes);
+    ptx::bulk_store(out + kTTBytes, smem + P::L_OFF, kTTBytes);
     ptx::bulk_commit_group();
-    ptx::bulk_wait_group_all();
+    ptx::bulk_wait_group_read<0>();
   }
   ptx::tc_fence_after();
   if (warp == 1) {
@@ -393,24 +573,47 @@ __global__ void __launch_bounds__(kPrepThreads)
 
 // -------------------------------------------------------------------- chain --
 
-constexpr int kChainThreads = 160;   // 4 compute warps, 1 warp that loads and issues MMAs
+constexpr int kPieces = 3;   // of S, X and U~
+constexpr int kCols = 16;    // columns of the block per compute thread
 
+// DVB columns of d_v per CTA. The three pieces of an operand lie side by side
+// on the N side, [hi | mid | lo], and the reader adds the three column blocks
+// of the result: an MMA with 128 rows takes the same 64 cycles (measured) for
+// any N up to 128, so one pass over three pieces of 32 columns costs what one
+// piece would. Compute threads hold one row, 16 columns wide (the splitting
+// stands on the critical path: 32 columns a thread took 400 cycles more per
+// operand); one more warp loads and issues the MMAs. S, X and U~ take turns in
+// one region, D1 and D3 in one set of tensor-memory columns: each is written
+// after the last reader of the one before it.
 template <int DK, int DVB>
 struct ChainCfg {
+  static constexpr int WARPS = 4 * (DVB / kCols);
+  static constexpr int THREADS = 32 * WARPS + 32;
   static constexpr int STAGE = kq_bytes(DK) + 2 * kTTBytes;
   static constexpr int S_PIECE = DK * DVB * 2;
   static constexpr int X_PIECE = C * DVB * 2;
-  static constexpr int S_OFF = 2 * STAGE;
-  static constexpr int X_OFF = S_OFF + 2 * S_PIECE;
-  static constexpr int U_OFF = X_OFF + 2 * X_PIECE;
-  static constexpr int BAR_OFF = U_OFF + 2 * X_PIECE;
+  static constexpr int R_OFF = 2 * STAGE;
+  static constexpr int BAR_OFF = R_OFF + kPieces * (S_PIECE > X_PIECE ? S_PIECE : X_PIECE);
   static constexpr int SMEM = 1024 + BAR_OFF + 128;
-  static constexpr uint32_t TMEM = 3 * DVB <= 128 ? 128 : 256;
-  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t D2_COL = kPieces * DVB;
+  static constexpr uint32_t TMEM = 2 * D2_COL <= 256 ? 256 : 512;
+  static_assert(SMEM <= 227 * 1024 && 2 * D2_COL <= TMEM, "shared and tensor memory per CTA");
 };
 
+// This thread's 16 columns of the three column blocks of a result, added.
+template <int DVB>
+__device__ __forceinline__ void ld_sum(uint32_t taddr, float (&x)[kCols]) {
+  float y[kCols], z[kCols];
+  ptx::tc_ld_32x32b_x16(taddr, x);
+  ptx::tc_ld_32x32b_x16(taddr + DVB, y);
+  ptx::tc_ld_32x32b_x16(taddr + 2 * DVB, z);
+  ptx::tc_wait_ld();
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) x[j] += y[j] + z[j];
+}
+
 template <int DK, int DVB>
-__global__ void __launch_bounds__(kChainThreads)
+__global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
     chain_kernel(const Args a) {
   using P = ChainCfg<DK, DVB>;
   extern __shared__ uint8_t smem_raw[];
@@ -433,12 +636,13 @@ __global__ void __launch_bounds__(kChainThreads)
   const int h = (blockIdx.x / blocks) % a.h_v;
   const int b = blockIdx.x / blocks / a.h_v;
   const int hk = h / (a.h_v / a.h_k);
+  constexpr int kMmaWarp = P::WARPS;
   if (t == 0) {
     ptx::mbar_init(&full[0], 1);
     ptx::mbar_init(&full[1], 1);
-    ptx::mbar_init(s_ready, 4);
-    ptx::mbar_init(x_ready, 2);
-    ptx::mbar_init(u_ready, 2);
+    ptx::mbar_init(s_ready, P::WARPS);
+    ptx::mbar_init(x_ready, P::WARPS);
+    ptx::mbar_init(u_ready, P::WARPS / 2);
     ptx::mbar_init(d1, 1);
     ptx::mbar_init(d2, 1);
     ptx::mbar_init(d3, 1);
@@ -446,7 +650,7 @@ __global__ void __launch_bounds__(kChainThreads)
     *abort_flag = 0u;
     ptx::fence_mbarrier_init();
   }
-  if (warp == 4) {
+  if (warp == kMmaWarp) {
     ptx::tmem_alloc(tmem_holder, P::TMEM);
     ptx::tmem_relinquish();
   }
@@ -462,7 +666,7 @@ __global__ void __launch_bounds__(kChainThreads)
   const int n = (end - start + C - 1) / C;
   const int slot0 = first_slot(start, b);
 
-  if (warp == 4) {
+  if (warp == kMmaWarp) {
     if (lane == 0) {
       auto load = [&](int c) {
         uint8_t* st = smem + (c & 1) * P::STAGE;
@@ -472,70 +676,65 @@ __global__ void __launch_bounds__(kChainThreads)
         ptx::bulk_load(st + kq_bytes(DK), a.tt + (cs * a.h_v + h) * kHeadBytes, 2 * kTTBytes,
                        &full[c & 1]);
       };
-      constexpr uint32_t kI1 = ptx::idesc_bf16(128, DVB, false, true);
-      constexpr uint32_t kI3 = ptx::idesc_bf16(128, DVB, true, true);
+      constexpr uint32_t kI1 = ptx::idesc_bf16(128, kPieces * DVB, false, true);
+      constexpr uint32_t kI2 = ptx::idesc_bf16(128, 2 * DVB, false, true);
+      constexpr uint32_t kI3 = ptx::idesc_bf16(128, kPieces * DVB, true, true);
       constexpr uint32_t kSN = DK * 16, kXN = C * 16;  // bytes between groups of 8 columns
+      const uint32_t r = sb + P::R_OFF;
       int loaded = 0, seen = 0;  // chunks requested; chunks whose load was waited for
       bool ok = true;
       if (n > 0) load(loaded++);
       for (int c = 0; c < n && ok; ++c) {
         const uint32_t par = c & 1;
         const uint32_t kq = sb + par * P::STAGE, tt = kq + kq_bytes(DK);
-        // S in place: the previous chunk's products, the last readers of the
-        // other stage, are complete
-        ok = skinny::wait_bounded(s_ready, par, abort_flag, kFaultChainMma);
-        if (!ok) break;
-        if (c + 1 < n) load(loaded++);
-        ok = skinny::wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma);
+        ok = wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma);
         if (!ok) break;
         ++seen;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int p = 0; p < 2; ++p)   // [K; Q] S
-#pragma unroll
-          for (int s = 0; s < DK / 16; ++s)
-            ptx::tc_mma_bf16(tmem, ptx::smem_desc(kq + (s / 4) * kHalfBytes + (s % 4) * 32, 16, 1024, 2),
-                             ptx::smem_desc(sb + P::S_OFF + p * P::S_PIECE + s * 256, 128, kSN, 0),
-                             kI1, (p | s) != 0);
-        ptx::tc_commit(d1);
-        ok = skinny::wait_bounded(x_ready, par, abort_flag, kFaultChainMma);
+        ok = wait_bounded(s_ready, par, abort_flag, kFaultChainMma);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t tp[3] = {0, 0, kTTBytes}, xp[3] = {0, P::X_PIECE, 0};
 #pragma unroll
-        for (int p = 0; p < 3; ++p)   // [T; AT] X
+        for (int s = 0; s < DK / 16; ++s)   // [K; Q] S
+          ptx::tc_mma_bf16(tmem, ptx::smem_desc(kq + (s / 4) * kHalfBytes + (s % 4) * 32, 16, 1024, 2),
+                           ptx::smem_desc(r + s * 256, 128, kSN, 0), kI1, s != 0);
+        ptx::tc_commit(d1);
+        // S in place means that the previous chunk's products, the last
+        // readers of the other stage, are complete
+        if (c + 1 < n) load(loaded++);
+        ok = wait_bounded(x_ready, par, abort_flag, kFaultChainMma);
+        if (!ok) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < 2; ++p)   // [T; AT] X: hi with all of X, lo with its hi and mid
 #pragma unroll
           for (int s = 0; s < C / 16; ++s)
-            ptx::tc_mma_bf16(tmem + DVB, ptx::smem_desc(tt + tp[p] + s * 32, 16, 1024, 2),
-                             ptx::smem_desc(sb + P::X_OFF + xp[p] + s * 256, 128, kXN, 0), kI1,
+            ptx::tc_mma_bf16(tmem + P::D2_COL, ptx::smem_desc(tt + p * kTTBytes + s * 32, 16, 1024, 2),
+                             ptx::smem_desc(r + s * 256, 128, kXN, 0), p == 0 ? kI1 : kI2,
                              (p | s) != 0);
         ptx::tc_commit(d2);
-        ok = skinny::wait_bounded(u_ready, par, abort_flag, kFaultChainMma);
+        ok = wait_bounded(u_ready, par, abort_flag, kFaultChainMma);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
-        for (int p = 0; p < 2; ++p)   // K^T U~ (64 of d_k: the upper rows repeat the lower)
-#pragma unroll
-          for (int s = 0; s < C / 16; ++s)
-            ptx::tc_mma_bf16(tmem + 2 * DVB,
-                             ptx::smem_desc(kq + s * 2048, DK == 128 ? kHalfBytes : 0, 1024, 2),
-                             ptx::smem_desc(sb + P::U_OFF + p * P::X_PIECE + s * 256, 128, kXN, 0),
-                             kI3, (p | s) != 0);
+        for (int s = 0; s < C / 16; ++s)   // K^T U~ (64 of d_k: the upper rows repeat the lower)
+          ptx::tc_mma_bf16(tmem, ptx::smem_desc(kq + s * 2048, DK == 128 ? kHalfBytes : 0, 1024, 2),
+                           ptx::smem_desc(r + s * 256, 128, kXN, 0), kI3, s != 0);
         ptx::tc_commit(d3);
       }
       if (!ok) {  // let what is in flight end before the CTA does
         ptx::tc_commit(drain);
-        skinny::drain_wait(drain, 0);
-        for (int c = seen; c < loaded; ++c) skinny::drain_wait(&full[c & 1], (c >> 1) & 1);
+        drain_wait(drain, 0);
+        for (int c = seen; c < loaded; ++c) drain_wait(&full[c & 1], (c >> 1) & 1);
       } else if (n > 0) {
-        skinny::drain_wait(d3, (n - 1) & 1);  // the last product, should the others give up on it
+        drain_wait(d3, (n - 1) & 1);  // the last product, should the others give up on it
       }
     }
   } else {
-    const int row = t & (C - 1);     // token of the chunk
-    const bool is_k = t < C;         // rows of K and U; else rows of Q and O
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    // the state: this thread holds row t of d_k
+    const int k_row = (warp & 3) * 32 + lane;   // row of d_k
+    const int row = k_row & (C - 1);            // token of the chunk
+    const bool is_k = (warp & 3) < 2;           // rows of K and U; else rows of Q and O
+    const int cols = (warp >> 2) * kCols;       // this thread's columns of the block
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + cols;
     int slot = -1;
     if (a.state != nullptr) {
       slot = a.slots != nullptr ? a.slots[b] : b;
@@ -546,100 +745,108 @@ __global__ void __launch_bounds__(kChainThreads)
         if (__any_sync(0xFFFFFFFFu, earlier)) slot = -1;
       }
     }
-    float* const state = a.state + ((static_cast<int64_t>(slot) * a.h_v + h) * DK + t) * a.d_v + c0;
-    float S[DVB];
+    const int64_t col = static_cast<int64_t>(h) * a.d_v + c0 + cols;  // column of V and O
+    float* const state = a.state + (static_cast<int64_t>(slot) * a.h_v * DK + k_row) * a.d_v +
+                         static_cast<int64_t>(h) * DK * a.d_v + c0 + cols;
+    float S[kCols];
 #pragma unroll
-    for (int j = 0; j < DVB; ++j) S[j] = 0.0f;
-    if (slot >= 0 && t < DK && a.resume != nullptr && a.resume[b] != 0) {
+    for (int j = 0; j < kCols; ++j) S[j] = 0.0f;
+    if (slot >= 0 && k_row < DK && a.resume != nullptr && a.resume[b] != 0) {
 #pragma unroll
-      for (int j = 0; j < DVB / 4; ++j) {
+      for (int j = 0; j < kCols / 4; ++j) {
         const float4 x = reinterpret_cast<const float4*>(state)[j];
         S[4 * j] = x.x; S[4 * j + 1] = x.y; S[4 * j + 2] = x.z; S[4 * j + 3] = x.w;
       }
     }
     const bool delta = a.beta != nullptr;
-    bool ok = true;
-    for (int c = 0; c < n; ++c) {
-      const uint32_t par = c & 1;
-      if (DK == 128 || t < DK)
-        store_row_split(sb + P::S_OFF, sb + P::S_OFF + P::S_PIECE, t, DK * 16, S);
-      ptx::fence_proxy_async_smem();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(s_ready);
+    // what the next chunk needs from memory, requested a chunk ahead
+    float eg = 0.0f, erest = 0.0f, bt = 0.0f, eall = 0.0f;
+    uint4 v[kCols / 8];
+    auto fetch = [&](int c) {
       const int64_t tok = start + static_cast<int64_t>(c) * C + row;
-      const bool live = tok < end;
       const float* gate = reinterpret_cast<const float*>(
           a.tt + (static_cast<int64_t>(slot0 + c) * a.h_v + h) * kHeadBytes + 2 * kTTBytes);
-      const float eg = gate[row], erest = gate[C + row], eall = gate[2 * C];
-      uint4 v[DVB / 8];
+      eg = gate[row];
+      erest = gate[C + row];
+      bt = gate[2 * C + row];
+      eall = gate[3 * C];
 #pragma unroll
-      for (int u = 0; u < DVB / 8; ++u) {
+      for (int u = 0; u < kCols / 8; ++u) {
         v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (is_k && live)
-          v[u] = *reinterpret_cast<const uint4*>(a.v + tok * a.ldv + static_cast<int64_t>(h) * a.d_v +
-                                                 c0 + 8 * u);
+        if (is_k && tok < end) v[u] = *reinterpret_cast<const uint4*>(a.v + tok * a.ldv + col + 8 * u);
       }
-      float D[DVB], inter[DVB];
+    };
+    auto arrive = [&](uint64_t* bar) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar);
+    };
+    auto publish = [&](uint64_t* bar) {  // operand rows written
+      ptx::fence_proxy_async_smem();
+      arrive(bar);
+    };
+    const uint32_t r_s = sb + P::R_OFF + (cols / 8) * (DK * 16);  // this thread's columns
+    const uint32_t r_x = sb + P::R_OFF + (cols / 8) * (C * 16);
+    bool ok = true;
+    if (n > 0) fetch(0);
+    for (int c = 0; c < n; ++c) {
+      const uint32_t par = c & 1;
+      if (DK == 128 || k_row < DK) store_row_split<kPieces>(r_s, P::S_PIECE, k_row, DK * 16, S);
+      publish(s_ready);
+      const int64_t tok = start + static_cast<int64_t>(c) * C + row;
+      const float eg_c = eg, erest_c = erest, eall_c = eall;
+      float D[kCols], Q[kCols];
       if (!(ok = warp_wait(d1, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      tc_ld(lanes, D);
+      ld_sum<DVB>(lanes, Q);
       if (is_k) {
 #pragma unroll
-        for (int u = 0; u < DVB / 8; ++u) {
+        for (int u = 0; u < kCols / 8; ++u) {
           const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = 8 * u + 2 * e;
             const float v0 = __uint_as_float(w[e] << 16), v1 = __uint_as_float(w[e] & 0xFFFF0000u);
-            D[j] = delta ? v0 - eg * D[j] : v0;
-            D[j + 1] = delta ? v1 - eg * D[j + 1] : v1;
+            D[j] = delta ? bt * (v0 - eg_c * Q[j]) : v0;
+            D[j + 1] = delta ? bt * (v1 - eg_c * Q[j + 1]) : v1;
           }
         }
-        store_row_split(sb + P::X_OFF, sb + P::X_OFF + P::X_PIECE, row, C * 16, D);
-        ptx::fence_proxy_async_smem();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(x_ready);
+        store_row_split<kPieces>(r_x, P::X_PIECE, row, C * 16, D);
+        publish(x_ready);
       } else {
-#pragma unroll
-        for (int j = 0; j < DVB; ++j) inter[j] = eg * D[j];
+        arrive(x_ready);  // Q S is taken: the product after next may go over it
       }
+      if (c + 1 < n) fetch(c + 1);
       if (!(ok = warp_wait(d2, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      tc_ld(lanes + DVB, D);
+      ld_sum<DVB>(lanes + P::D2_COL, D);
       if (is_k) {
 #pragma unroll
-        for (int j = 0; j < DVB; ++j) D[j] *= erest;
-        store_row_split(sb + P::U_OFF, sb + P::U_OFF + P::X_PIECE, row, C * 16, D);
-        ptx::fence_proxy_async_smem();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(u_ready);
-      } else if (live) {
-        __nv_bfloat16* o = a.o + tok * a.ldo + static_cast<int64_t>(h) * a.d_v + c0;
+        for (int j = 0; j < kCols; ++j) D[j] *= erest_c;
+        store_row_split<kPieces>(r_x, P::X_PIECE, row, C * 16, D);
+        publish(u_ready);
+      } else if (tok < end) {
+        __nv_bfloat16* o = a.o + tok * a.ldo + col;
 #pragma unroll
-        for (int u = 0; u < DVB / 8; ++u) {
+        for (int u = 0; u < kCols / 8; ++u) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = 8 * u + 2 * e;
-            const __nv_bfloat162 p = __floats2bfloat162_rn(a.scale * (inter[j] + D[j]),
-                                                           a.scale * (inter[j + 1] + D[j + 1]));
-            w[e] = *reinterpret_cast<const uint32_t*>(&p);
+            w[e] = round_piece(a.scale * (eg_c * Q[j] + D[j]), a.scale * (eg_c * Q[j + 1] + D[j + 1]));
           }
           *reinterpret_cast<uint4*>(o + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       if (!(ok = warp_wait(d3, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      tc_ld(lanes + 2 * DVB, D);
+      ld_sum<DVB>(lanes, D);
 #pragma unroll
-      for (int j = 0; j < DVB; ++j) S[j] = eall * S[j] + D[j];
+      for (int j = 0; j < kCols; ++j) S[j] = eall_c * S[j] + D[j];
     }
-    if (ok && slot >= 0 && t < DK) {
+    if (ok && slot >= 0 && k_row < DK) {
 #pragma unroll
-      for (int j = 0; j < DVB / 4; ++j)
+      for (int j = 0; j < kCols / 4; ++j)
         reinterpret_cast<float4*>(state)[j] =
             make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
     }
@@ -647,7 +854,7 @@ __global__ void __launch_bounds__(kChainThreads)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 4) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     ptx::tmem_dealloc(tmem, P::TMEM);
   }

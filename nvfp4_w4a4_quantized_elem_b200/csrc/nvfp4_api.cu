@@ -1251,7 +1251,7 @@ nvfp4_status launch_chain(DeviceState* st, unsigned bit, const nvfp4::la::Args& 
   const int64_t grid = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / DVB);
   if (grid >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
   if (nvfp4_status e = la_smem(st, bit, chain_kernel<DK, DVB>, Cfg::SMEM)) return e;
-  return launch_pdl(chain_kernel<DK, DVB>, static_cast<unsigned>(grid), kChainThreads, Cfg::SMEM, s,
+  return launch_pdl(chain_kernel<DK, DVB>, static_cast<unsigned>(grid), Cfg::THREADS, Cfg::SMEM, s,
                     1u, a);
 }
 
@@ -1265,7 +1265,13 @@ nvfp4_status launch_linear_attention(DeviceState* st, const nvfp4::la::Args& a, 
   if (nvfp4_status e = launch_pdl(prepare_kernel<DK>, static_cast<unsigned>(grid), kPrepThreads,
                                   PrepCfg<DK>::SMEM, s, 1u, a))
     return e;
-  return launch_chain<DK, 32>(st, base + 1, a, s);
+  // Columns of d_v per CTA: 32 keep a chunk's step short (2.5 us against 3.7 us
+  // with 64, 8192 tokens of 32 heads as one prompt: 320 against 479 us) while
+  // there are few CTAs; from several waves on, 64 do more per step (23 ragged
+  // prompts of 48 heads, 7.6 K tokens: 440 against 557 us).
+  const int64_t waves64 = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / 64) / st->sms;
+  return a.d_v % 64 == 0 && waves64 >= 4 ? launch_chain<DK, 64>(st, base + 2, a, s)
+                                         : launch_chain<DK, 32>(st, base + 1, a, s);
 }
 
 }  // namespace

@@ -8,6 +8,7 @@ raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -110,13 +111,18 @@ def _check(status: int, what: str) -> None:
         raise NVFP4Error(what, status)
 
 
-def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+# A call of a few microseconds on the GPU waits for the host otherwise: plain
+# integers go through ctypes as they are, and the current stream is asked for
+# by its handle (torch.cuda.current_stream() builds an object, ~3 us).
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream: torch.cuda.Stream | None) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream: torch.cuda.Stream | None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    torch.cuda.init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _require_cuda(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> None:
@@ -387,44 +393,43 @@ def silu_mul(y: torch.Tensor, out: torch.Tensor | None = None,
 def _heads(q, k, v, decay, beta, state, out):
     """Checked arguments shared by linear_attention and its step: (h_k, h_v,
     d_k, d_v, row pitches of q, k, v and out, out)."""
-    for t, name, dt in ((q, "q", torch.bfloat16), (k, "k", torch.bfloat16),
-                        (v, "v", torch.bfloat16), (decay, "decay", torch.float32),
-                        (beta, "beta", torch.float32), (state, "state", torch.float32),
-                        (out, "out", torch.bfloat16)):
-        if t is not None:
-            _require_cuda(t, name, dt)
-            if t.device != q.device:
-                raise ValueError(f"{name} must be on {q.device}")
-    if q.device.index != torch.cuda.current_device():
-        raise ValueError(f"q is on {q.device}, the current device is {torch.cuda.current_device()}")
-    if q.dim() != 3 or v.dim() != 3 or q.shape != k.shape or v.shape[0] != q.shape[0]:
-        raise ValueError("q and k must be [rows, h_k, d_k], v [rows, h_v, d_v]")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"q is on {dev}, the current device is {torch.cuda.current_device()}")
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+        if t is not None and (t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 3):
+            raise ValueError(f"{name} must be {torch.bfloat16} [rows, heads, dim] on {dev}")
     rows, hk, dk = q.shape
     _, hv, dv = v.shape
-    for t, name in ((decay, "decay"), (beta, "beta")):
-        if t is not None and (tuple(t.shape) != (rows, hv) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous [{rows}, {hv}]")
-    if state is not None and (state.dim() != 4 or tuple(state.shape[1:]) != (hv, dk, dv)
-                              or not state.is_contiguous()):
-        raise ValueError(f"state must be contiguous [slots, {hv}, {dk}, {dv}]")
+    if k.shape != q.shape or v.shape[0] != rows:
+        raise ValueError("q and k must be [rows, h_k, d_k], v [rows, h_v, d_v]")
+    for t, name, shape in ((decay, "decay", (rows, hv)), (beta, "beta", (rows, hv)),
+                           (state, "state", (hv, dk, dv))):
+        if t is None:
+            continue
+        if t.dtype != torch.float32 or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {torch.float32} on {dev}")
+        if (t.shape[1:] if t is state else t.shape) != shape:
+            raise ValueError(f"{name} must be {'[slots] + ' if t is state else ''}{list(shape)}")
     if out is None:
-        out = torch.empty((rows, hv, dv), dtype=torch.bfloat16, device=q.device)
-    elif tuple(out.shape) != (rows, hv, dv):
+        out = torch.empty((rows, hv, dv), dtype=torch.bfloat16, device=dev)
+    elif out.shape != v.shape:
         raise ValueError(f"out must be [{rows}, {hv}, {dv}]")
     pitches = []
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        h, d = t.shape[1], t.shape[2]
-        if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
-            raise ValueError(f"the heads of a row of {name} must be contiguous")
-        pitches.append(t.stride(0) if rows > 1 else -(-h * d // 8) * 8)
+    for t, h, d in ((q, hk, dk), (k, hk, dk), (v, hv, dv), (out, hv, dv)):
+        ld, head, one = t.stride()
+        if (d > 1 and one != 1) or (h > 1 and head != d):
+            raise ValueError("the heads of a row of q, k, v and out must be contiguous")
+        pitches.append(ld if rows > 1 else -(-h * d // 8) * 8)
     return hk, hv, dk, dv, pitches, out
 
 
 def _int32(t: torch.Tensor | None, name: str, n: int, device) -> None:
     if t is not None:
-        _require_cuda(t, name, torch.int32)
-        if tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} must be a contiguous vector of {n} on {device}")
+        if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be a contiguous {torch.int32} vector of {n} on {device}")
 
 
 def linear_attention_workspace_bytes(total: int, n_seq: int, h_k: int, h_v: int, d_k: int) -> int:
@@ -452,9 +457,9 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
     _int32(slots, "slots", n_seq, q.device)
     _int32(resume, "resume", n_seq, q.device)
     if workspace is None:
-        with torch.cuda.stream(stream):
-            workspace = torch.empty(linear_attention_workspace_bytes(total, n_seq, hk, hv, dk),
-                                    dtype=torch.uint8, device=q.device)
+        need = linear_attention_workspace_bytes(total, n_seq, hk, hv, dk)
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     st = lib().nvfp4_linear_attention(
         _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(decay), _ptr(beta),
         dk ** -0.5 if scale is None else scale, total, hk, hv, dk, dv, n_seq, _ptr(cu_seqlens),

@@ -269,7 +269,7 @@ nvfp4_status nvfp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx,
                           size_t workspace_bytes, nvfp4_stream_t stream);
 
 /* Activations of the GEMM epilogue, evaluated in FP32:
- *   RELU max(z, 0);  SILU z / (1 + e^-z);  GELU z/2 erfc(-z / sqrt 2);
+ *   RELU max(z, 0);  SILU z / (1 + e^-z);  GELU z/2 (1 + erf(z / sqrt 2));
  *   GELU_TANH z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
 typedef enum {
   NVFP4_ACT_NONE = 0,

@@ -6,7 +6,7 @@
 // product; the epilogue is the model's own and is written from the formulas:
 //   relu       max(z, 0)
 //   silu       z / (1 + e^-z)
-//   gelu       z/2 erfc(-z / sqrt 2)
+//   gelu       z/2 (1 + erf(z / sqrt 2))
 //   gelu_tanh  z/2 (1 + tanh u) = z / (1 + e^-2u), u = sqrt(2/pi) (z + 0.044715 z^3)
 // Without the fusion the bf16 product makes one more round trip through
 // memory per step (2 m n bytes written, read and written again) and is
@@ -15,6 +15,8 @@
 
 #include <cuda_bf16.h>
 #include <cstdint>
+
+#include "ptx.cuh"
 
 namespace nvfp4 {
 namespace epi {
@@ -28,19 +30,23 @@ struct Args {
   int act;
 };
 
-// z / (1 + e^t). The fast exponential and division (a few FP32 ulp) serve
-// every finite z: where e^t leaves the fast division's range (above 2^126) or
-// overflows, the quotient is given as 0 and the true value is below 1e-35.
-__device__ __forceinline__ float over_one_plus_exp(float z, float t) {
-  return __fdividef(z, 1.0f + __expf(t));
+// z / (1 + 2^t), two instructions of the special-function unit. Where 2^t
+// overflows or its reciprocal is subnormal (t > 126) the quotient is given as
+// 0; the true value is below 1e-35.
+__device__ __forceinline__ float over_one_plus_ex2(float z, float t) {
+  return z * ptx::rcp(1.0f + ptx::ex2(t));
 }
 
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if (ACT == kRelu) return fmaxf(z, 0.0f);
-  if (ACT == kSilu) return over_one_plus_exp(z, -z);
-  if (ACT == kGelu) return 0.5f * z * erfcf(-0.70710678f * z);
-  if (ACT == kGeluTanh) return over_one_plus_exp(z, -1.59576912f * (z + 0.044715f * z * z * z));
+  if (ACT == kSilu) return over_one_plus_ex2(z, -1.44269504f * z);
+  if (ACT == kGelu) {  // erff: 2 ulp; erfcf would keep the far tail's digits at 4x the time
+    const float h = 0.5f * z;
+    return fmaf(h, erff(0.70710678f * z), h);
+  }
+  if (ACT == kGeluTanh)  // -2u log2(e) = z (-2.30220819 - 0.102943240 z^2)
+    return over_one_plus_ex2(z, z * fmaf(z * z, -0.102943240f, -2.30220819f));
   return z;
 }
 
@@ -87,28 +93,74 @@ __device__ __forceinline__ uint4 load_bf16x8(const __nv_bfloat16* p, int left) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 32 consecutive columns of one output row: acc (FP32 bits) -> y (FP32 bits).
-// bias32: shared-memory copy of the columns' bias (null without a bias), the
-// same addresses for the whole warp; res: this row's residual at the first
-// column, or null; left: columns of the row from the first on. All residual
-// loads come first; the arithmetic goes 8 columns at a time, so that a thread
-// which holds 128 accumulator columns stays inside its 168 registers.
-__device__ __forceinline__ void apply32(uint32_t (&acc)[32], float alpha, int act,
-                                        const uint16_t* bias32, const __nv_bfloat16* res,
-                                        int left) {
-  uint4 rv[4];
+// The residual of a chunk of 32 rows x 32 columns, held by a warp as it is
+// loaded: four lanes per row, 16 bytes each, so that every sector that comes
+// from L2 is used whole (a lane per row, 16 bytes at a time, fetched them
+// twice: the L1 that the GEMM's shared memory leaves does not hold 16 warps'
+// lines). exchange() hands each lane its own row by way of the warp's 2 KiB
+// staging chunk, in the layout that the output goes through it.
+struct ResChunk {
+  uint4 v[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* res, int64_t ld, int rows, int cols,
+                                       int lane) {
+    const int u = lane & 3, left = cols - 8 * u;
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
-    rv[u] = res != nullptr && left > 8 * u ? load_bf16x8(res + 8 * u, left - 8 * u)
-                                           : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      v[i] = r < rows && left > 0 ? load_bf16x8(res + r * ld + 8 * u, left)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void exchange(uint8_t* chunk, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), u = lane & 3;
+      *reinterpret_cast<uint4*>(chunk + r * 64 + ((u ^ ((r >> 1) & 3)) << 4)) = v[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      v[u] = *reinterpret_cast<const uint4*>(chunk + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4));
+  }
+};
+
+// 32 consecutive columns of one output row, acc (FP32 bits) in place:
+// act(acc alpha + bias). bias32: shared-memory copy of the columns' bias (null
+// without one), the same addresses for the whole warp.
+template <int ACT>
+__device__ __forceinline__ void apply32_as(uint32_t (&acc)[32], float alpha,
+                                           const uint16_t* bias32) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     float z[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(acc[8 * u + i]) * alpha;
     if (bias32 != nullptr) add_bf16x8(z, *reinterpret_cast<const uint4*>(bias32 + 8 * u));
-    activate_n(act, z);
-    add_bf16x8(z, rv[u]);
+    activate_all<ACT>(z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[8 * u + i] = __float_as_uint(z[i]);
+  }
+}
+
+__device__ __forceinline__ void apply32(uint32_t (&acc)[32], float alpha, int act,
+                                        const uint16_t* bias32) {
+  switch (act) {
+    case kRelu: apply32_as<kRelu>(acc, alpha, bias32); break;
+    case kSilu: apply32_as<kSilu>(acc, alpha, bias32); break;
+    case kGelu: apply32_as<kGelu>(acc, alpha, bias32); break;
+    case kGeluTanh: apply32_as<kGeluTanh>(acc, alpha, bias32); break;
+    default: apply32_as<kNone>(acc, alpha, bias32); break;
+  }
+}
+
+// The exchanged residual added to them.
+__device__ __forceinline__ void add_residual(uint32_t (&acc)[32], const ResChunk& r) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(acc[8 * u + i]);
+    add_bf16x8(z, r.v[u]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[8 * u + i] = __float_as_uint(z[i]);
   }

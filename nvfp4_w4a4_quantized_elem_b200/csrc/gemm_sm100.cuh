@@ -59,12 +59,13 @@
 // as it reduces the amax pass's partials: the output is that of the unfused
 // chain (GEMM -> bf16 gate/up -> silu*mul -> dynamic quantization of h).
 // Epilogue arguments (EPI instantiation, plain output only): bias, activation
-// and residual (epilogue.cuh) are applied to the FP32 accumulator, after the
-// slices' sum where K is split. The tile's bias is staged per warp in shared
-// memory before the accumulator is ready; a thread owns one output row, so
-// its residual comes in four 16-byte loads per 32 columns, behind the
-// accumulator's release and so beside the next tile's MMAs. A separate
-// instantiation: the plain kernel keeps its registers and its results.
+// and residual (epilogue.cuh) on the FP32 accumulator, after the slices' sum
+// where K is split. 16 epilogue warps of 64 columns instead of 8 of 128 (and
+// one staging chunk each instead of two): the arithmetic and the residual's
+// latency have to fit beside the next tile's MMAs, and 128 accumulator columns
+// leave a thread no registers for them. Bias and residual of a tile are asked
+// for while its MMAs run. The plain kernel is a separate instantiation and
+// keeps its registers and results.
 // Launched with programmatic stream serialisation: barrier set-up and
 // tensor-memory allocation overlap the previous kernel in the stream; the
 // producer and the epilogue wait for it before touching global memory, except
@@ -103,7 +104,6 @@ constexpr int NUM_EPI_WARPS = 8;
 constexpr int SF_WARP0 = 2;                   // warps 2, 3: scale copies
 constexpr int NUM_SF_WARPS = 2;
 constexpr int EPI_WARP0 = SF_WARP0 + NUM_SF_WARPS;  // warps 4..11
-constexpr int NUM_THREADS = 32 * EPI_WARP0 + 32 * NUM_EPI_WARPS;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t ACC_COL = 0;               // [0, 256): FP32 accumulator
 constexpr int NSF = STAGES;                   // tensor-memory scale buffers, one per stage
@@ -115,10 +115,15 @@ constexpr int EPI_WARP_BYTES = 2 * EPI_CHUNK_BYTES;
 constexpr int EPI_OFF = STAGES * STAGE_BYTES;  // staging tiles after the ring
 constexpr int BAR_OFF = EPI_OFF + NUM_EPI_WARPS * EPI_WARP_BYTES;
 constexpr int RTAB_OFF = BAR_OFF + 512;      // fused mode: g_h / dec(s) for 128 codes
-constexpr int BIAS_OFF = RTAB_OFF + 512;     // EPI: 128 bf16 of bias per epilogue warp
-constexpr int BIAS_WARP_BYTES = 128 * 2;
-constexpr size_t SMEM_BYTES =
-    1024 + static_cast<size_t>(BIAS_OFF) + NUM_EPI_WARPS * BIAS_WARP_BYTES;
+constexpr int BIAS_OFF = RTAB_OFF + 512;     // EPI: 2 x 2 x 128 bf16 of bias
+constexpr size_t SMEM_BYTES = 1024 + static_cast<size_t>(BIAS_OFF) + 1024;
+// EPI instantiation: twice the warps, each with one staging chunk
+template <bool EPI>
+struct Epilogue {
+  static constexpr int WARPS = EPI ? 2 * NUM_EPI_WARPS : NUM_EPI_WARPS;
+  static constexpr int THREADS = 32 * EPI_WARP0 + 32 * WARPS;
+  static constexpr int CHUNKS = EPI ? 1 : 2;  // staging chunks per warp
+};
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
 constexpr uint64_t kDrainLimitNs = 100000000ull;  // 0.1 s for the abort drain
@@ -399,7 +404,7 @@ __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t ssfa, uint32
 }
 
 template <bool EPI>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(Epilogue<EPI>::THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSFA,
                 const __grid_constant__ CUtensorMap tmSFB,
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ptx::mbar_init(&sf_landed[s], 1);
     }
     ptx::mbar_init(tmem_full, 1);
-    ptx::mbar_init(tmem_empty, 2 * NUM_EPI_WARPS);
+    ptx::mbar_init(tmem_empty, 2 * Epilogue<EPI>::WARPS);
     ptx::mbar_init(drain, 1);
     for (int b = 0; b < NSF; ++b) {
       ptx::mbar_init(&sf_full[b], NUM_SF_WARPS);
@@ -667,16 +672,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * NUM_EPI_WARPS) : "memory");
     }
     const int q = warp & 3;                     // tensor-memory lane quarter
-    const int half = (warp - EPI_WARP0) >> 2;   // accumulator columns [128*half, +128)
+    constexpr int kChunks = Epilogue<EPI>::CHUNKS;
+    const int half = (warp - EPI_WARP0) >> (EPI ? 3 : 2);  // accumulator columns [128*half, +128)
     const float alpha = 1.0f / (__ldg(p.a_global) * __ldg(p.b_global));
     const uint32_t release = ptx::mapa_shared(ptx::smem_u32(tmem_empty), 0);
-    uint8_t* const stage_tiles = smem + EPI_OFF + (warp - EPI_WARP0) * EPI_WARP_BYTES;
-    uint32_t nchunk = 0;  // chunks this warp has handed to the TMA (buffer = nchunk & 1)
+    uint8_t* const stage_tiles = smem + EPI_OFF + (warp - EPI_WARP0) * kChunks * EPI_CHUNK_BYTES;
+    uint32_t nchunk = 0;  // chunks this warp has handed to the TMA (buffer = nchunk % kChunks)
     // Hand one staged chunk to the TMA once the buffer's previous store has
     // finished reading it.
     auto emit = [&](auto&& fill, int x, int y) {
-      uint8_t* buf = stage_tiles + (nchunk & 1u) * EPI_CHUNK_BYTES;
-      if (lane == 0) ptx::bulk_wait_group_read<1>();
+      uint8_t* buf = stage_tiles + (nchunk % kChunks) * EPI_CHUNK_BYTES;
+      if (lane == 0) ptx::bulk_wait_group_read<kChunks - 1>();
       __syncwarp();
       fill(ptx::smem_u32(buf));
       ptx::fence_proxy_async_smem();
@@ -693,30 +699,126 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Unit unit = unit_of(t, p);
       int mb, nb;
       tile_coords(unit.tile, p, mb, nb);
-      uint16_t* const bias_tile = reinterpret_cast<uint16_t*>(
-          smem + BIAS_OFF + (warp - EPI_WARP0) * BIAS_WARP_BYTES);
-      if (EPI && p.epi.bias != nullptr) {  // this warp's 128 columns, 4 per lane
-        const int c0 = nb * BN + half * 128 + 4 * lane;
-        const uint16_t* b = reinterpret_cast<const uint16_t*>(p.epi.bias) + c0;
-        uint32_t w0 = 0u, w1 = 0u;
-        if (c0 + 4 <= p.N) {
-          const uint2 v = *reinterpret_cast<const uint2*>(b);
-          w0 = v.x;
-          w1 = v.y;
-        } else {
-          if (c0 < p.N) w0 = b[0];
-          if (c0 + 1 < p.N) w0 |= static_cast<uint32_t>(b[1]) << 16;
-          if (c0 + 2 < p.N) w1 = b[2];
+      const int row0 = mb * BM + static_cast<int>(rank) * HALF + q * 32;  // this warp's rows
+      if (EPI) {
+        const int part = ((warp - EPI_WARP0) >> 2) & 1;  // this warp's 64 of the half's columns
+        const int col0 = nb * BN + half * 128;           // the half's first column
+        // while the tile's MMAs run: the half's bias, 4 columns per lane, and
+        // the first residual chunk
+        uint2 bw = make_uint2(0u, 0u);
+        if (p.epi.bias != nullptr) {
+          const int c0 = col0 + 4 * lane;
+          const uint16_t* b = reinterpret_cast<const uint16_t*>(p.epi.bias) + c0;
+          if (c0 + 4 <= p.N) {
+            bw = *reinterpret_cast<const uint2*>(b);
+          } else {
+            if (c0 < p.N) bw.x = b[0];
+            if (c0 + 1 < p.N) bw.x |= static_cast<uint32_t>(b[1]) << 16;
+            if (c0 + 2 < p.N) bw.y = b[2];
+          }
         }
-        __syncwarp();  // the previous tile's reads are over
-        reinterpret_cast<uint2*>(bias_tile)[lane] = make_uint2(w0, w1);
+        // residual of the half's columns [32 cc, +32)
+        const bool has_res = p.epi.residual != nullptr;
+        epi::ResChunk res;
+        auto load_res = [&](int cc) {
+          if (has_res)
+            res.load(p.epi.residual + static_cast<int64_t>(row0) * p.epi.ldr + col0 + 32 * cc,
+                     p.epi.ldr, p.M - row0, p.N - col0 - 32 * cc, lane);
+        };
+        load_res(2 * part);
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(tmem_full, acc_phase, ab, kFaultEpilogue))) break;
+        ptx::tc_fence_after();
+        uint32_t r0[32], r1[32];
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + ACC_COL +
+                               half * 128u + part * 64u;
+        ptx::tc_ld_32x32b_x32(taddr, r0);
+        ptx::tc_ld_32x32b_x32(taddr + 32u, r1);
+        ptx::tc_wait_ld();
+        ptx::tc_fence_before();
         __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(release);
+        // Bias to shared memory, every warp of a half the same bytes, in the
+        // buffer of this unit's parity: whoever could still read that buffer
+        // (two units back) has since released an accumulator that this unit's
+        // MMAs waited for.
+        uint16_t* const bias_tile =
+            reinterpret_cast<uint16_t*>(smem + BIAS_OFF) + (acc_phase * 2 + half) * 128;
+        if (p.epi.bias != nullptr) {
+          reinterpret_cast<uint2*>(bias_tile)[lane] = bw;
+          __syncwarp();
+        }
+        acc_phase ^= 1u;
+        if (row0 >= p.M) continue;  // warp-uniform; rows past M inside are clipped by the TMA
+        // columns [32 cc, +32) of the half, then the residual of chunk `then`
+        auto put = [&](uint32_t(&acc)[32], int cc, int then) {
+          epi::apply32(acc, alpha, p.epi.act,
+                       p.epi.bias != nullptr ? bias_tile + 32 * cc : nullptr);
+          if (has_res) {
+            if (lane == 0) ptx::bulk_wait_group_read<0>();
+            __syncwarp();
+            res.exchange(stage_tiles, lane);
+            epi::add_residual(acc, res);
+            if (then >= 0) load_res(then);
+          }
+          const int c = col0 + 32 * cc;
+          if (!p.y_fp32) {
+            emit([&](uint32_t b) { stage_bf16(b, lane, acc, 1.0f); }, c, row0);
+          } else {
+            emit([&](uint32_t b) { stage_f32(b, lane, acc, 0, 1.0f); }, c, row0);
+            emit([&](uint32_t b) { stage_f32(b, lane, acc, 16, 1.0f); }, c + 16, row0);
+          }
+        };
+        if (p.split > 1) {
+          // as the plain kernel's split, but a region's two warps count the
+          // slices of their 64 columns apart, in the halves of its counter
+          const int region = static_cast<int>(rank) * 8 + half * 4 + q;
+          const int64_t slab_stride = int64_t{16} * kRegionFloats;  // one slice of a tile
+          float* const base = p.partial + int64_t{unit.tile} * p.split * slab_stride +
+                              int64_t{region} * kRegionFloats;
+          float4* mine = reinterpret_cast<float4*>(base + unit.slice * slab_stride) + lane +
+                         32 * 16 * part;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            __stcg(mine + 32 * c, make_float4(__uint_as_float(r0[4 * c]), __uint_as_float(r0[4 * c + 1]),
+                                              __uint_as_float(r0[4 * c + 2]),
+                                              __uint_as_float(r0[4 * c + 3])));
+            __stcg(mine + 32 * (8 + c),
+                   make_float4(__uint_as_float(r1[4 * c]), __uint_as_float(r1[4 * c + 1]),
+                               __uint_as_float(r1[4 * c + 2]), __uint_as_float(r1[4 * c + 3])));
+          }
+          __threadfence();
+          __syncwarp();
+          unsigned int* cnt = p.tile_count + unit.tile * 16 + region;
+          const int field = 16 * part;
+          uint32_t last = 0;
+          if (lane == 0)
+            last = ((atomicAdd(cnt, 1u << field) >> field) & 0xFFFFu) ==
+                   static_cast<unsigned>(p.split - 1);
+          last = __shfl_sync(0xFFFFFFFFu, last, 0);
+          if (!last) continue;
+          __threadfence();
+          for (int cc = 2 * part; cc < 2 * part + 2; ++cc) {
+            const float4* src = reinterpret_cast<const float4*>(base) + lane + 32 * (8 * cc);
+            switch (p.split) {
+              case 2: sum_slices<2>(src, slab_stride / 4, r0); break;
+              case 3: sum_slices<3>(src, slab_stride / 4, r0); break;
+              default: sum_slices<kMaxSplitK>(src, slab_stride / 4, r0); break;
+            }
+            put(r0, cc, cc == 2 * part ? cc + 1 : -1);
+          }
+          // ready for the next call
+          if (lane == 0) atomicSub(cnt, static_cast<unsigned>(p.split) << field);
+          continue;
+        }
+        put(r0, 2 * part, 2 * part + 1);
+        put(r1, 2 * part + 1, -1);
+        continue;
       }
       // warp-uniform: no lane may leave while the others go on to the
       // warp-wide tensor-memory loads
       if (!__all_sync(0xFFFFFFFFu, wait_bounded(tmem_full, acc_phase, ab, kFaultEpilogue))) break;
       ptx::tc_fence_after();
-      if (!EPI && p.fused == kFusedBf16Amax) {
+      if (p.fused == kFusedBf16Amax) {
         // gate columns [64 half, +64) and the matching up columns (+128) ->
         // 64 bf16 h columns of 32 rows, two TMA-stored chunks
         uint32_t g0[32], g1[32], u0[32], u1[32];
@@ -730,14 +832,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster(release);
         acc_phase ^= 1u;
-        const int row0 = mb * BM + static_cast<int>(rank) * HALF + q * 32;
         if (row0 >= p.M) continue;  // rows past M inside are zero (h = 0) and clipped
         const int hc0 = nb * 128 + 64 * half;
         emit([&](uint32_t b) { stage_h(b, lane, g0, u0, alpha, h_amax); }, hc0, row0);
         emit([&](uint32_t b) { stage_h(b, lane, g1, u1, alpha, h_amax); }, hc0 + 32, row0);
         continue;
       }
-      if (!EPI && p.fused == kFusedQuantStatic) {
+      if (p.fused == kFusedQuantStatic) {
         // gate columns [64 half, +64) and the matching up columns (+128)
         uint32_t g0[32], g1[32], u0[32], u1[32];
         const uint32_t lb = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64u * half;
@@ -783,18 +884,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) ptx::mbar_arrive_cluster(release);
       acc_phase ^= 1u;
 
-      const int row0 = mb * BM + static_cast<int>(rank) * HALF + q * 32;  // this warp's rows
       const int col0 = nb * BN + half * 128;
-      // EPI: columns [32 cc, +32) of this thread's row, in place; alpha is then spent
-      const __nv_bfloat16* res_row = nullptr;
-      if (EPI && p.epi.residual != nullptr && row0 + lane < p.M)
-        res_row = p.epi.residual + static_cast<int64_t>(row0 + lane) * p.epi.ldr + col0;
-      auto finish = [&](uint32_t(&acc)[32], int cc) {
-        epi::apply32(acc, alpha, p.epi.act,
-                     p.epi.bias != nullptr ? bias_tile + 32 * cc : nullptr,
-                     res_row != nullptr ? res_row + 32 * cc : nullptr, p.N - col0 - 32 * cc);
-      };
-      const float beta = EPI ? 1.0f : alpha;  // scale left to the staging
       if (p.split > 1) {
         // rows past M (a tile's padding): no partial, no count, no output
         if (row0 >= p.M) continue;
@@ -837,12 +927,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             case 3: sum_slices<3>(src, slab_stride / 4, acc); break;
             default: sum_slices<kMaxSplitK>(src, slab_stride / 4, acc); break;
           }
-          if (EPI) finish(acc, cc);
           if (!p.y_fp32) {
-            emit([&](uint32_t b) { stage_bf16(b, lane, acc, beta); }, col0 + 32 * cc, row0);
+            emit([&](uint32_t b) { stage_bf16(b, lane, acc, alpha); }, col0 + 32 * cc, row0);
           } else {
-            emit([&](uint32_t b) { stage_f32(b, lane, acc, 0, beta); }, col0 + 32 * cc, row0);
-            emit([&](uint32_t b) { stage_f32(b, lane, acc, 16, beta); }, col0 + 32 * cc + 16,
+            emit([&](uint32_t b) { stage_f32(b, lane, acc, 0, alpha); }, col0 + 32 * cc, row0);
+            emit([&](uint32_t b) { stage_f32(b, lane, acc, 16, alpha); }, col0 + 32 * cc + 16,
                  row0);
           }
         }
@@ -850,19 +939,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         continue;
       }
       if (row0 >= p.M) continue;  // warp-uniform; rows past M inside are clipped by the TMA
-      auto put = [&](uint32_t(&acc)[32], int cc) {
-        if (EPI) finish(acc, cc);
-        if (!p.y_fp32) {
-          emit([&](uint32_t b) { stage_bf16(b, lane, acc, beta); }, col0 + 32 * cc, row0);
-        } else {
-          emit([&](uint32_t b) { stage_f32(b, lane, acc, 0, beta); }, col0 + 32 * cc, row0);
-          emit([&](uint32_t b) { stage_f32(b, lane, acc, 16, beta); }, col0 + 32 * cc + 16, row0);
-        }
-      };
-      put(r0, 0);
-      put(r1, 1);
-      put(r2, 2);
-      put(r3, 3);
+      if (!p.y_fp32) {
+        emit([&](uint32_t b) { stage_bf16(b, lane, r0, alpha); }, col0 + 0, row0);
+        emit([&](uint32_t b) { stage_bf16(b, lane, r1, alpha); }, col0 + 32, row0);
+        emit([&](uint32_t b) { stage_bf16(b, lane, r2, alpha); }, col0 + 64, row0);
+        emit([&](uint32_t b) { stage_bf16(b, lane, r3, alpha); }, col0 + 96, row0);
+      } else {
+        emit([&](uint32_t b) { stage_f32(b, lane, r0, 0, alpha); }, col0 + 0, row0);
+        emit([&](uint32_t b) { stage_f32(b, lane, r0, 16, alpha); }, col0 + 16, row0);
+        emit([&](uint32_t b) { stage_f32(b, lane, r1, 0, alpha); }, col0 + 32, row0);
+        emit([&](uint32_t b) { stage_f32(b, lane, r1, 16, alpha); }, col0 + 48, row0);
+        emit([&](uint32_t b) { stage_f32(b, lane, r2, 0, alpha); }, col0 + 64, row0);
+        emit([&](uint32_t b) { stage_f32(b, lane, r2, 16, alpha); }, col0 + 80, row0);
+        emit([&](uint32_t b) { stage_f32(b, lane, r3, 0, alpha); }, col0 + 96, row0);
+        emit([&](uint32_t b) { stage_f32(b, lane, r3, 16, alpha); }, col0 + 112, row0);
+      }
     }
     if (lane == 0) ptx::bulk_wait_group_all();  // stores done before the CTA can exit
     if (!EPI && p.fused == kFusedBf16Amax) {

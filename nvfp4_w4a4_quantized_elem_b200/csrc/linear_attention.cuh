@@ -328,13 +328,6 @@ __device__ __forceinline__ void invert_unit_lower(const float* L, float* T, floa
   invert_diagonal<3, 4>(L, T, M, t);
 }
 
-// 2^x, zero below 2^-126.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // x[j] *= f e^{G_t - G_j} for j <= last, zero beyond (a score that is not
 // finite, too). Without branches: a branch per block of columns puts x into
 // local memory.
@@ -344,8 +337,8 @@ __device__ __forceinline__ void decay_row(float (&x)[C], const float2* G, int ro
 #pragma unroll
   for (int j = 0; j < C; j += 2) {
     const float4 g = *reinterpret_cast<const float4*>(G + j);
-    const float e0 = f * ex2((gt.x - g.x) + (gt.y - g.y));
-    const float e1 = f * ex2((gt.x - g.z) + (gt.y - g.w));
+    const float e0 = f * ptx::ex2((gt.x - g.x) + (gt.y - g.y));
+    const float e1 = f * ptx::ex2((gt.x - g.z) + (gt.y - g.w));
     x[j] = j <= last ? e0 * x[j] : 0.0f;
     x[j + 1] = j + 1 <= last ? e1 * x[j + 1] : 0.0f;
   }
@@ -487,10 +480,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     const float2 gt = G[row], ge = G[C - 1];
     const float f = Beta[row];
     float* gate = reinterpret_cast<float*>(out + 2 * kTTBytes);
-    gate[row] = ex2(gt.x + gt.y);
-    gate[C + row] = ex2((ge.x - gt.x) + (ge.y - gt.y));
+    gate[row] = ptx::ex2(gt.x + gt.y);
+    gate[C + row] = ptx::ex2((ge.x - gt.x) + (ge.y - gt.y));
     gate[2 * C + row] = f;
-    if (row == 0) gate[3 * C] = ex2(ge.x + ge.y);
+    if (row == 0) gate[3 * C] = ptx::ex2(ge.x + ge.y);
     if (delta) {
       decay_row(x, G, row, row - 1, f);
 #pragma unroll

@@ -768,7 +768,8 @@ nvfp4_status gemm_paired(PFN_cuTensorMapEncodeTiled_v12000 enc, DeviceState* st,
   const int64_t max_pairs = st->sms / 2;
   const int pairs = static_cast<int>(units < max_pairs ? units : max_pairs);
   if (grid_out != nullptr) *grid_out = 2 * pairs;
-  return launch_pdl(kernel, static_cast<unsigned>(2 * pairs), NUM_THREADS, SMEM_BYTES,
+  return launch_pdl(kernel, static_cast<unsigned>(2 * pairs),
+                    ep ? Epilogue<true>::THREADS : Epilogue<false>::THREADS, SMEM_BYTES,
                     stream, 2u, tmA, tmB, tmSFA, tmSFB, tmY, p);
 }
 

@@ -47,6 +47,19 @@ __device__ __forceinline__ float e4m3_value(uint32_t s) {
   return e == 0 ? sub : normal;
 }
 
+// 2^x (2 ulp) and 1/x (1 ulp); subnormal inputs and results are zero.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---------------------------------------------------------------- mbarrier --
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {

@@ -25,13 +25,14 @@
 // sequence's chunks in order, one CTA per (sequence, head, d_v block), with S
 // in FP32 registers.
 //
-// Precision: q, k, v are bf16 and enter the products exactly. The FP32 operands
-// S, X and U~ are cut into three bf16 pieces (24 bits, nothing is lost), T and
-// A T into two (2^-17 of them is lost, but T's unit diagonal, beta standing in
-// X, is exact); products are accumulated in FP32. One bf16 operand alone would
-// leave 2^-9 in the FP32 states. G is summed in FP64 and kept as two FP32
-// parts: the difference of two FP32 sums of strong decays would lose the weak
-// decays between them.
+// Precision: q, k, v are bf16 and enter the products exactly. FP32 operands are
+// cut into bf16 pieces, products accumulated in FP32. X and U~, on which the
+// FP32 states rest directly, take three pieces (24 bits, nothing is lost); S,
+// which returns into the state only through beta K S, and T and A T, whose unit
+// diagonal is exact, take two (2^-18 of the value is lost). One bf16 operand
+// alone would leave 2^-9 in the states. G is summed in FP64 and kept as two
+// FP32 parts: the difference of two FP32 sums of strong decays would lose the
+// weak decays between them.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -102,10 +103,17 @@ __device__ __forceinline__ uint32_t take_piece(float& x, float& y) {
   return __byte_perm(a, b, 0x7632);
 }
 
-// The last of two pieces is rounded instead: 2^-17 of the value is left.
+// Two pieces are rounded instead: 2^-18 of the value is left.
 __device__ __forceinline__ uint32_t round_piece(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t take_rounded(float& x, float& y) {
+  const uint32_t w = round_piece(x, y);
+  x -= __uint_as_float(w << 16);
+  y -= __uint_as_float(w & 0xFFFF0000u);
+  return w;
 }
 
 // Row `k` of an MN-major operand without swizzle (8 x 16-byte core matrices,
@@ -129,8 +137,8 @@ __device__ __forceinline__ void store_row_split(uint32_t base, int piece, int k,
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        w[e] = PIECES == 2 && p == 1 ? round_piece(r[2 * e], r[2 * e + 1])
-                                     : take_piece(r[2 * e], r[2 * e + 1]);
+        w[e] = PIECES == 2 ? take_rounded(r[2 * e], r[2 * e + 1])
+                           : take_piece(r[2 * e], r[2 * e + 1]);
       ptx::st_shared_v4(at + p * piece, w[0], w[1], w[2], w[3]);
     }
   }
@@ -152,8 +160,7 @@ __device__ __forceinline__ void store_image_row(uint32_t base, int piece, int r,
     for (int p = 0; p < 2; ++p) {
       uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = p == 1 ? round_piece(v[2 * e], v[2 * e + 1]) : take_piece(v[2 * e], v[2 * e + 1]);
+      for (int e = 0; e < 4; ++e) w[e] = take_rounded(v[2 * e], v[2 * e + 1]);
       ptx::st_shared_v4(base + p * piece + sw128(r, u), w[0], w[1], w[2], w[3]);
     }
   }
@@ -566,61 +573,70 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 
 // -------------------------------------------------------------------- chain --
 
-constexpr int kPieces = 3;   // of S, X and U~
-constexpr int kCols = 16;    // columns of the block per compute thread
+constexpr int kSPieces = 2, kPieces = 3;   // of S; of X and U~
+constexpr int DVB = 32;                    // columns of d_v per CTA
+constexpr int kCols = 16;                  // of them per compute thread
 
-// DVB columns of d_v per CTA. The three pieces of an operand lie side by side
-// on the N side, [hi | mid | lo], and the reader adds the three column blocks
-// of the result: an MMA with 128 rows takes the same 64 cycles (measured) for
-// any N up to 128, so one pass over three pieces of 32 columns costs what one
-// piece would. Compute threads hold one row, 16 columns wide (the splitting
-// stands on the critical path: 32 columns a thread took 400 cycles more per
-// operand); one more warp loads and issues the MMAs. S, X and U~ take turns in
-// one region, D1 and D3 in one set of tensor-memory columns: each is written
-// after the last reader of the one before it.
-template <int DK, int DVB>
+// The pieces of an operand lie side by side on the N side, [hi | mid | lo], and
+// the reader adds the column blocks of the result: an MMA with 128 rows and K
+// = 16 takes 30 cycles for 32 columns and 50 for 96 (measured), behind ~300
+// cycles from its issue to the arrival of its commit, so pieces in N cost less
+// than pieces one after the other. Compute threads hold one row, 16 columns
+// wide (the splitting stands on the critical path: 32 columns a thread took 400
+// cycles more per operand); one more warp loads and issues the MMAs.
+// A step of one chunk is a chain of latencies (4.4 K cycles, 1.2 K of them in
+// MMAs), so two CTAs share an SM and fill each other's gaps; for that the
+// shared memory is cut to half an SM's: S, X and U~ take turns in one region,
+// [T; AT] has one buffer (reloaded behind its product, two products ahead of
+// its next use), only [K; Q] two. D1 and D3 share tensor-memory columns. 64
+// columns per CTA and one CTA per SM took 6.8 K cycles per step.
+template <int DK>
 struct ChainCfg {
   static constexpr int WARPS = 4 * (DVB / kCols);
   static constexpr int THREADS = 32 * WARPS + 32;
-  static constexpr int STAGE = kq_bytes(DK) + 2 * kTTBytes;
   static constexpr int S_PIECE = DK * DVB * 2;
   static constexpr int X_PIECE = C * DVB * 2;
-  static constexpr int R_OFF = 2 * STAGE;
-  static constexpr int BAR_OFF = R_OFF + kPieces * (S_PIECE > X_PIECE ? S_PIECE : X_PIECE);
-  static constexpr int SMEM = 1024 + BAR_OFF + 128;
+  static constexpr int TT_OFF = 2 * kq_bytes(DK);
+  static constexpr int R_OFF = TT_OFF + 2 * kTTBytes;
+  static constexpr int R_BYTES = kSPieces * S_PIECE > kPieces * X_PIECE ? kSPieces * S_PIECE
+                                                                        : kPieces * X_PIECE;
+  static constexpr int BAR_OFF = R_OFF + R_BYTES;
+  static constexpr int SMEM = BAR_OFF + 128;   // the base is 1024-byte aligned
   static constexpr uint32_t D2_COL = kPieces * DVB;
-  static constexpr uint32_t TMEM = 2 * D2_COL <= 256 ? 256 : 512;
-  static_assert(SMEM <= 227 * 1024 && 2 * D2_COL <= TMEM, "shared and tensor memory per CTA");
+  static constexpr uint32_t TMEM = 256;
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024 && 2 * D2_COL <= TMEM, "two CTAs per SM");
 };
 
-// This thread's 16 columns of the three column blocks of a result, added.
-template <int DVB>
+// This thread's 16 columns of the BLOCKS column blocks of a result, added.
+template <int BLOCKS>
 __device__ __forceinline__ void ld_sum(uint32_t taddr, float (&x)[kCols]) {
-  float y[kCols], z[kCols];
+  float y[BLOCKS - 1][kCols];
   ptx::tc_ld_32x32b_x16(taddr, x);
-  ptx::tc_ld_32x32b_x16(taddr + DVB, y);
-  ptx::tc_ld_32x32b_x16(taddr + 2 * DVB, z);
+#pragma unroll
+  for (int i = 0; i < BLOCKS - 1; ++i) ptx::tc_ld_32x32b_x16(taddr + (i + 1) * DVB, y[i]);
   ptx::tc_wait_ld();
 #pragma unroll
-  for (int j = 0; j < kCols; ++j) x[j] += y[j] + z[j];
+  for (int j = 0; j < kCols; ++j)
+#pragma unroll
+    for (int i = 0; i < BLOCKS - 1; ++i) x[j] += y[i][j];
 }
 
-template <int DK, int DVB>
-__global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
+template <int DK>
+__global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
     chain_kernel(const Args a) {
-  using P = ChainCfg<DK, DVB>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);  // [2] stage loaded
+  using P = ChainCfg<DK>;
+  extern __shared__ __align__(1024) uint8_t smem_chain[];
+  uint8_t* const smem = smem_chain;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);  // [2] K; Q loaded
   uint64_t* const s_ready = full + 2;   // operand pieces written by the compute warps
   uint64_t* const x_ready = full + 3;
   uint64_t* const u_ready = full + 4;
   uint64_t* const d1 = full + 5;        // products complete
   uint64_t* const d2 = full + 6;
   uint64_t* const d3 = full + 7;
-  uint64_t* const drain = full + 8;
-  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(full + 9);
+  uint64_t* const full_tt = full + 8;   // T; AT loaded
+  uint64_t* const drain = full + 9;
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(full + 10);
   volatile uint32_t* const abort_flag = tmem_holder + 1;
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -639,8 +655,11 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
     ptx::mbar_init(d1, 1);
     ptx::mbar_init(d2, 1);
     ptx::mbar_init(d3, 1);
+    ptx::mbar_init(full_tt, 1);
     ptx::mbar_init(drain, 1);
-    *abort_flag = 0u;
+    // the swizzled images need the alignment that the declaration asks for
+    *abort_flag = (ptx::smem_u32(smem) & 1023u) != 0u ? 1u : 0u;
+    if (*abort_flag) atomicOr(&g_fault_word, kFaultChain);
     ptx::fence_mbarrier_init();
   }
   if (warp == kMmaWarp) {
@@ -661,28 +680,36 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
 
   if (warp == kMmaWarp) {
     if (lane == 0) {
-      auto load = [&](int c) {
-        uint8_t* st = smem + (c & 1) * P::STAGE;
-        const int64_t cs = slot0 + c;
-        ptx::mbar_arrive_expect_tx(&full[c & 1], P::STAGE);
-        ptx::bulk_load(st, a.kq + (cs * a.h_k + hk) * kq_bytes(DK), kq_bytes(DK), &full[c & 1]);
-        ptx::bulk_load(st + kq_bytes(DK), a.tt + (cs * a.h_v + h) * kHeadBytes, 2 * kTTBytes,
-                       &full[c & 1]);
+      auto load_kq = [&](int c) {
+        ptx::mbar_arrive_expect_tx(&full[c & 1], kq_bytes(DK));
+        ptx::bulk_load(smem + (c & 1) * kq_bytes(DK),
+                       a.kq + ((static_cast<int64_t>(slot0) + c) * a.h_k + hk) * kq_bytes(DK),
+                       kq_bytes(DK), &full[c & 1]);
       };
-      constexpr uint32_t kI1 = ptx::idesc_bf16(128, kPieces * DVB, false, true);
-      constexpr uint32_t kI2 = ptx::idesc_bf16(128, 2 * DVB, false, true);
+      auto load_tt = [&](int c) {
+        ptx::mbar_arrive_expect_tx(full_tt, 2 * kTTBytes);
+        ptx::bulk_load(smem + P::TT_OFF,
+                       a.tt + ((static_cast<int64_t>(slot0) + c) * a.h_v + h) * kHeadBytes,
+                       2 * kTTBytes, full_tt);
+      };
+      constexpr uint32_t kI1 = ptx::idesc_bf16(128, kSPieces * DVB, false, true);
+      constexpr uint32_t kI2 = ptx::idesc_bf16(128, kPieces * DVB, false, true);
+      constexpr uint32_t kI2lo = ptx::idesc_bf16(128, 2 * DVB, false, true);
       constexpr uint32_t kI3 = ptx::idesc_bf16(128, kPieces * DVB, true, true);
       constexpr uint32_t kSN = DK * 16, kXN = C * 16;  // bytes between groups of 8 columns
-      const uint32_t r = sb + P::R_OFF;
-      int loaded = 0, seen = 0;  // chunks requested; chunks whose load was waited for
-      bool ok = true;
-      if (n > 0) load(loaded++);
+      const uint32_t r = sb + P::R_OFF, tt = sb + P::TT_OFF;
+      int kq_asked = 0, kq_seen = 0, tt_asked = 0, tt_seen = 0;  // chunks
+      bool ok = *abort_flag == 0u;
+      if (n > 0 && ok) {
+        load_kq(kq_asked++);
+        load_tt(tt_asked++);
+      }
       for (int c = 0; c < n && ok; ++c) {
         const uint32_t par = c & 1;
-        const uint32_t kq = sb + par * P::STAGE, tt = kq + kq_bytes(DK);
+        const uint32_t kq = sb + par * kq_bytes(DK);
         ok = wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma);
         if (!ok) break;
-        ++seen;
+        ++kq_seen;
         ok = wait_bounded(s_ready, par, abort_flag, kFaultChainMma);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -692,8 +719,11 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
                            ptx::smem_desc(r + s * 256, 128, kSN, 0), kI1, s != 0);
         ptx::tc_commit(d1);
         // S in place means that the previous chunk's products, the last
-        // readers of the other stage, are complete
-        if (c + 1 < n) load(loaded++);
+        // readers of the other buffer, are complete
+        if (c + 1 < n) load_kq(kq_asked++);
+        ok = wait_bounded(full_tt, par, abort_flag, kFaultChainMma);
+        if (!ok) break;
+        ++tt_seen;
         ok = wait_bounded(x_ready, par, abort_flag, kFaultChainMma);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -702,7 +732,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
 #pragma unroll
           for (int s = 0; s < C / 16; ++s)
             ptx::tc_mma_bf16(tmem + P::D2_COL, ptx::smem_desc(tt + p * kTTBytes + s * 32, 16, 1024, 2),
-                             ptx::smem_desc(r + s * 256, 128, kXN, 0), p == 0 ? kI1 : kI2,
+                             ptx::smem_desc(r + s * 256, 128, kXN, 0), p == 0 ? kI2 : kI2lo,
                              (p | s) != 0);
         ptx::tc_commit(d2);
         ok = wait_bounded(u_ready, par, abort_flag, kFaultChainMma);
@@ -713,11 +743,13 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
           ptx::tc_mma_bf16(tmem, ptx::smem_desc(kq + s * 2048, DK == 128 ? kHalfBytes : 0, 1024, 2),
                            ptx::smem_desc(r + s * 256, 128, kXN, 0), kI3, s != 0);
         ptx::tc_commit(d3);
+        if (c + 1 < n) load_tt(tt_asked++);  // U~ in place means [T; AT] X complete
       }
       if (!ok) {  // let what is in flight end before the CTA does
         ptx::tc_commit(drain);
         drain_wait(drain, 0);
-        for (int c = seen; c < loaded; ++c) drain_wait(&full[c & 1], (c >> 1) & 1);
+        for (int c = kq_seen; c < kq_asked; ++c) drain_wait(&full[c & 1], (c >> 1) & 1);
+        if (tt_seen < tt_asked) drain_wait(full_tt, tt_seen & 1);
       } else if (n > 0) {
         drain_wait(d3, (n - 1) & 1);  // the last product, should the others give up on it
       }
@@ -784,14 +816,14 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
     if (n > 0) fetch(0);
     for (int c = 0; c < n; ++c) {
       const uint32_t par = c & 1;
-      if (DK == 128 || k_row < DK) store_row_split<kPieces>(r_s, P::S_PIECE, k_row, DK * 16, S);
+      if (DK == 128 || k_row < DK) store_row_split<kSPieces>(r_s, P::S_PIECE, k_row, DK * 16, S);
       publish(s_ready);
       const int64_t tok = start + static_cast<int64_t>(c) * C + row;
       const float eg_c = eg, erest_c = erest, eall_c = eall;
       float D[kCols], Q[kCols];
       if (!(ok = warp_wait(d1, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      ld_sum<DVB>(lanes, Q);
+      ld_sum<kSPieces>(lanes, Q);
       if (is_k) {
 #pragma unroll
         for (int u = 0; u < kCols / 8; ++u) {
@@ -812,7 +844,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
       if (c + 1 < n) fetch(c + 1);
       if (!(ok = warp_wait(d2, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      ld_sum<DVB>(lanes + P::D2_COL, D);
+      ld_sum<kPieces>(lanes + P::D2_COL, D);
       if (is_k) {
 #pragma unroll
         for (int j = 0; j < kCols; ++j) D[j] *= erest_c;
@@ -833,7 +865,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 1)
       }
       if (!(ok = warp_wait(d3, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      ld_sum<DVB>(lanes, D);
+      ld_sum<kPieces>(lanes, D);
 #pragma unroll
       for (int j = 0; j < kCols; ++j) S[j] = eall_c * S[j] + D[j];
     }

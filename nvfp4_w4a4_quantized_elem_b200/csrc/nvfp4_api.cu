@@ -1245,34 +1245,26 @@ nvfp4_status la_smem(DeviceState* st, unsigned bit, K kernel, int bytes) {
   return NVFP4_OK;
 }
 
-template <int DK, int DVB>
-nvfp4_status launch_chain(DeviceState* st, unsigned bit, const nvfp4::la::Args& a, cudaStream_t s) {
-  using namespace nvfp4::la;
-  using Cfg = ChainCfg<DK, DVB>;
-  const int64_t grid = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / DVB);
-  if (grid >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
-  if (nvfp4_status e = la_smem(st, bit, chain_kernel<DK, DVB>, Cfg::SMEM)) return e;
-  return launch_pdl(chain_kernel<DK, DVB>, static_cast<unsigned>(grid), Cfg::THREADS, Cfg::SMEM, s,
-                    1u, a);
-}
-
 template <int DK>
 nvfp4_status launch_linear_attention(DeviceState* st, const nvfp4::la::Args& a, cudaStream_t s) {
   using namespace nvfp4::la;
-  const unsigned base = DK == 128 ? 0u : 4u;
-  const int64_t grid = chunk_slots(a.total, a.n_seq) * a.h_v;
-  if (grid >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
+  using Chain = ChainCfg<DK>;
+  constexpr int kAloneSmem = 120 * 1024;
+  static_assert(Chain::SMEM <= kAloneSmem, "chain_kernel's shared memory");
+  const unsigned base = DK == 128 ? 0u : 2u;
+  const int64_t prep = chunk_slots(a.total, a.n_seq) * a.h_v;
+  const int64_t chain = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / DVB);
+  if (prep >= (int64_t{1} << 31) || chain >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
   if (nvfp4_status e = la_smem(st, base, prepare_kernel<DK>, PrepCfg<DK>::SMEM)) return e;
-  if (nvfp4_status e = launch_pdl(prepare_kernel<DK>, static_cast<unsigned>(grid), kPrepThreads,
+  if (nvfp4_status e = la_smem(st, base + 1, chain_kernel<DK>, kAloneSmem)) return e;
+  if (nvfp4_status e = launch_pdl(prepare_kernel<DK>, static_cast<unsigned>(prep), kPrepThreads,
                                   PrepCfg<DK>::SMEM, s, 1u, a))
     return e;
-  // Columns of d_v per CTA: 32 keep a chunk's step short (2.5 us against 3.7 us
-  // with 64, 8192 tokens of 32 heads as one prompt: 320 against 479 us) while
-  // there are few CTAs; from several waves on, 64 do more per step (23 ragged
-  // prompts of 48 heads, 7.6 K tokens: 440 against 557 us).
-  const int64_t waves64 = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / 64) / st->sms;
-  return a.d_v % 64 == 0 && waves64 >= 4 ? launch_chain<DK, 64>(st, base + 2, a, s)
-                                         : launch_chain<DK, 32>(st, base + 1, a, s);
+  // At most one CTA per SM's worth: asking for more than half of an SM's shared
+  // memory keeps them apart (they start while the first kernel's CTAs leave, and
+  // two on one SM then took 8192 tokens of 32 heads from 447 to 561 us).
+  const int smem = chain <= st->sms ? kAloneSmem : Chain::SMEM;
+  return launch_pdl(chain_kernel<DK>, static_cast<unsigned>(chain), Chain::THREADS, smem, s, 1u, a);
 }
 
 }  // namespace

@@ -149,10 +149,13 @@ __device__ __forceinline__ uint32_t sw128(int r, int u) {
   return static_cast<uint32_t>(r * 128 + ((u ^ (r & 7)) << 4));
 }
 
-// 64 FP32 values of row r -> hi and lo images of the rows (`piece` apart).
-__device__ __forceinline__ void store_image_row(uint32_t base, int piece, int r, const float* x) {
+// N FP32 values of row r, from its 16-byte unit u0 on -> hi and lo images of the
+// rows (`piece` apart).
+template <int N>
+__device__ __forceinline__ void store_image_row(uint32_t base, int piece, int r, int u0,
+                                                const float (&x)[N]) {
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
+  for (int u = 0; u < N / 8; ++u) {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = x[8 * u + e];
@@ -161,7 +164,7 @@ __device__ __forceinline__ void store_image_row(uint32_t base, int piece, int r,
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = take_rounded(v[2 * e], v[2 * e + 1]);
-      ptx::st_shared_v4(base + p * piece + sw128(r, u), w[0], w[1], w[2], w[3]);
+      ptx::st_shared_v4(base + p * piece + sw128(r, u0 + u), w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -213,17 +216,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
 
 // ------------------------------------------------------------------ prepare --
 
-constexpr int kPrepThreads = 128;
+constexpr int kPrepThreads = 256;
 constexpr int kLd = 68;                       // row pitch (floats) of the 64x64 tiles
 constexpr int kTileBytes = C * kLd * 4;
-constexpr int kMLd = 20;                      // row pitch of the inverse's 16x16 scratch
-constexpr int kMBytes = 16 * kMLd * 4;
+constexpr int kMLd = 36;                      // row pitch of the inverse's 32x32 scratch
+constexpr int kMBytes = 32 * kMLd * 4;
 
 // Shared memory: the [K; Q] image, over which L and T = (I + L)^-1 are written
 // once the scores are taken; T's pieces go over L, the two pieces of the
 // [T; AT] image over T and, the product A T done, over T's pieces. A's pieces
 // are the rows 64..127 of 128-row operands whose rows 0..63 lie in whatever
-// stands before them: those rows of the product are not read.
+// stands before them: those rows of the product are not read. Four CTAs of 256
+// threads per SM: the kernel is a chain of short dependent phases, and what
+// fills their gaps is other CTAs.
 template <int DK>
 struct PrepCfg {
   static constexpr int KQ = kq_bytes(DK);
@@ -233,83 +238,62 @@ struct PrepCfg {
   static constexpr int A_PIECE = kTTBytes / 2;
   static constexpr int G_OFF = A_OFF + 2 * A_PIECE;        // G, beta
   static constexpr int M_OFF = G_OFF + C * 8 + C * 4;      // scratch of the inverse
-  static constexpr int BAR_OFF = M_OFF + 3 * kMBytes;
-  static constexpr int SMEM = 1024 + BAR_OFF + 64;
-  static_assert(KQ <= A_OFF && kTTBytes <= kTileBytes && kTileBytes % 1024 == 0, "regions");
+  static constexpr int BAR_OFF = M_OFF + kMBytes;
+  static constexpr int SMEM = BAR_OFF + 64;                // the base is 1024-byte aligned
+  static_assert(KQ <= A_OFF && kTTBytes <= kTileBytes && kTileBytes % 1024 == 0 &&
+                4 * (SMEM + 1024) <= 228 * 1024, "regions, four CTAs per SM");
 };
 
-// acc[i][4] (+)= rows r0 + 8 i of A times B, 16 x 16 blocks of pitch lda, ldb;
-// this thread's columns c4 .. c4 + 3.
-template <int NR>
-__device__ __forceinline__ void block_mac(float (&acc)[NR][4], const float* A, int lda,
-                                          const float* B, int ldb, int r0, int c4) {
-#pragma unroll
-  for (int m = 0; m < 16; m += 4) {
-    float4 a[NR], b[4];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) a[i] = *reinterpret_cast<const float4*>(A + (r0 + 8 * i) * lda + m);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (m + j) * ldb + c4);
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const float av[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][0] += av[j] * b[j].x;
-        acc[i][1] += av[j] * b[j].y;
-        acc[i][2] += av[j] * b[j].z;
-        acc[i][3] += av[j] * b[j].w;
-      }
-    }
+// acc (16x8, FP32) += A (16 x 8 KS, row-major) B (8 KS x 8, row-major) by
+// mma.sync.m16n8k8 on tf32: FP32 values as two tf32 pieces each, products
+// hi hi + hi lo + lo hi (2^-21 of the operands' product is lost). The fragment
+// loads are single words, 32 banks (A) or 16 (B) at a time.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4],
+                                         const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+__device__ __forceinline__ void tile_mac(float (&acc)[4], const float* A, int lda, const float* B,
+                                         int ldb, int steps, int lane) {
+  const int g = lane >> 2, q = lane & 3;
+  for (int k = 0; k < 8 * steps; k += 8) {
+    uint32_t ah[4], al[4], bh[2], bl[2];
+    split_tf32(A[g * lda + k + q], ah[0], al[0]);
+    split_tf32(A[(g + 8) * lda + k + q], ah[1], al[1]);
+    split_tf32(A[g * lda + k + q + 4], ah[2], al[2]);
+    split_tf32(A[(g + 8) * lda + k + q + 4], ah[3], al[3]);
+    split_tf32(B[(k + q) * ldb + g], bh[0], bl[0]);
+    split_tf32(B[(k + q + 4) * ldb + g], bh[1], bl[1]);
+    mma_tf32(acc, al, bh);
+    mma_tf32(acc, ah, bl);
+    mma_tf32(acc, ah, bh);
   }
 }
 
-// Blocks of T = (I + L)^-1 D block diagonals below the main one: T_ij =
-// -T_ii sum_{j <= m < i} L_im T_mj for i = j + D, WPB warps per block (16/WPB
-// rows each). M: one 16x16 scratch per block.
-template <int D, int WPB>
-__device__ __forceinline__ void invert_diagonal(const float* L, float* T, float* M, int t) {
-  constexpr int NB = 4 - D, RW = 16 / WPB, NR = RW >= 16 ? 2 : 1;
-  const int warp = t >> 5, lane = t & 31;
-  const int blk = warp / WPB, j = blk, i = j + D;
-  const int c4 = (lane & 3) * 4, r0 = (warp % WPB) * RW + (lane >> 2);
-  const bool on = blk < NB && (lane >> 2) < RW;
-  float* const m = M + blk * 16 * kMLd;
-  float acc[NR][4];
-  auto clear = [&] {
-#pragma unroll
-    for (int a = 0; a < NR; ++a)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) acc[a][b] = 0.0f;
-  };
-  if (on) {
-    clear();
-#pragma unroll
-    for (int k = 0; k < D; ++k)
-      block_mac<NR>(acc, L + 16 * i * kLd + 16 * (j + k), kLd, T + 16 * (j + k) * kLd + 16 * j, kLd, r0, c4);
-#pragma unroll
-    for (int a = 0; a < NR; ++a)
-      *reinterpret_cast<float4*>(m + (r0 + 8 * a) * kMLd + c4) =
-          make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
-  }
-  __syncthreads();
-  if (on) {
-    clear();
-    block_mac<NR>(acc, T + 16 * i * kLd + 16 * i, kLd, m, kMLd, r0, c4);
-#pragma unroll
-    for (int a = 0; a < NR; ++a)
-      *reinterpret_cast<float4*>(T + (16 * i + r0 + 8 * a) * kLd + 16 * j + c4) =
-          make_float4(-acc[a][0], -acc[a][1], -acc[a][2], -acc[a][3]);
-  }
-  __syncthreads();
+__device__ __forceinline__ void tile_store(float* D, int ld, const float (&acc)[4], float sign,
+                                           int lane) {
+  const int g = lane >> 2, c = 2 * (lane & 3);
+  *reinterpret_cast<float2*>(D + g * ld + c) = make_float2(sign * acc[0], sign * acc[1]);
+  *reinterpret_cast<float2*>(D + (g + 8) * ld + c) = make_float2(sign * acc[2], sign * acc[3]);
 }
 
-// T = (I + L)^-1 for the strictly lower triangular L, in FP32 by 16x16 blocks:
-// the diagonal ones by forward substitution, one thread per column, then one
-// block diagonal after the other. 87 K multiply-adds per chunk and head, on
-// the FP32 units: as split bf16 products the 16-wide blocks would spend more on
-// splitting and moving operands than on arithmetic.
+// T = (I + L)^-1 for the strictly lower triangular L: the 16x16 diagonal blocks
+// by FP32 forward substitution, one thread per column, then twice
+// [P 0; B Q]^-1 = [P^-1 0; -Q^-1 B P^-1 Q^-1], with 16- and 32-wide blocks on split
+// tf32 tiles, one 16x8 tile a warp, zero k-steps of the triangles left out. (On
+// the FP32 units these products read shared memory 16 bytes a lane for every
+// few multiply-adds and were what bounded the whole kernel: 73% of the shared
+// memory's bandwidth.) T's 16x16 blocks above the diagonal are not written.
 __device__ __forceinline__ void invert_unit_lower(const float* L, float* T, float* M, int t) {
+  const int warp = t >> 5, lane = t & 31;
   if (t < C) {
     const int b0 = t & ~15, j = t & 15;
     float x[16];
@@ -319,7 +303,7 @@ __device__ __forceinline__ void invert_unit_lower(const float* L, float* T, floa
 #pragma unroll
       for (int m = 0; m < i; m += 4) {
         const float4 l = *reinterpret_cast<const float4*>(L + (b0 + i) * kLd + b0 + m);
-        s[0] -= l.x * x[m];  // L is zero from the diagonal on
+        s[0] -= l.x * x[m];
         if (m + 1 < i) s[1] -= l.y * x[m + 1];
         if (m + 2 < i) s[2] -= l.z * x[m + 2];
         if (m + 3 < i) s[3] -= l.w * x[m + 3];
@@ -330,24 +314,50 @@ __device__ __forceinline__ void invert_unit_lower(const float* L, float* T, floa
     for (int i = 0; i < 16; ++i) T[(b0 + i) * kLd + b0 + j] = x[i];
   }
   __syncthreads();
-  invert_diagonal<1, 1>(L, T, M, t);
-  invert_diagonal<2, 2>(L, T, M, t);
-  invert_diagonal<3, 4>(L, T, M, t);
+  {
+    // blocks (1, 0) and (3, 2), two tiles of 8 columns each, by warps 0..3
+    const int o = 32 * (warp >> 1), c = 8 * (warp & 1);
+    float* const m = M + 16 * kMLd * (warp >> 1);
+    if (warp < 4) {
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      tile_mac(acc, L + (o + 16) * kLd + o, kLd, T + o * kLd + o + c, kLd, 2, lane);
+      tile_store(m + c, kMLd, acc, 1.0f, lane);
+    }
+    __syncthreads();
+    if (warp < 4) {
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      tile_mac(acc, T + (o + 16) * kLd + o + 16, kLd, m + c, kMLd, 2, lane);
+      tile_store(T + (o + 16) * kLd + o + c, kLd, acc, -1.0f, lane);
+    }
+    __syncthreads();
+  }
+  {
+    // the 32x32 block below: row tile i, column tile j
+    const int i = warp >> 2, j = warp & 3;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    tile_mac(acc, L + (32 + 16 * i) * kLd + 8 * j, kLd, T + 8 * j * kLd + 8 * j, kLd, 4 - j, lane);
+    tile_store(M + 16 * i * kMLd + 8 * j, kMLd, acc, 1.0f, lane);
+    __syncthreads();
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+    tile_mac(acc, T + (32 + 16 * i) * kLd + 32, kLd, M + 8 * j, kMLd, 2 + 2 * i, lane);
+    tile_store(T + (32 + 16 * i) * kLd + 8 * j, kLd, acc, -1.0f, lane);
+    __syncthreads();
+  }
 }
 
-// x[j] *= f e^{G_t - G_j} for j <= last, zero beyond (a score that is not
-// finite, too). Without branches: a branch per block of columns puts x into
-// local memory.
-__device__ __forceinline__ void decay_row(float (&x)[C], const float2* G, int row, int last,
-                                          float f) {
+// x[j] (column j0 + j) *= f e^{G_t - G_j} up to column `last`, zero beyond (a
+// score that is not finite, too). Without branches: a branch per block of
+// columns puts x into local memory.
+__device__ __forceinline__ void decay_row(float (&x)[32], const float2* G, int row, int j0,
+                                          int last, float f) {
   const float2 gt = G[row];
 #pragma unroll
-  for (int j = 0; j < C; j += 2) {
-    const float4 g = *reinterpret_cast<const float4*>(G + j);
+  for (int j = 0; j < 32; j += 2) {
+    const float4 g = *reinterpret_cast<const float4*>(G + j0 + j);
     const float e0 = f * ptx::ex2((gt.x - g.x) + (gt.y - g.y));
     const float e1 = f * ptx::ex2((gt.x - g.z) + (gt.y - g.w));
-    x[j] = j <= last ? e0 * x[j] : 0.0f;
-    x[j + 1] = j + 1 <= last ? e1 * x[j + 1] : 0.0f;
+    x[j] = j0 + j <= last ? e0 * x[j] : 0.0f;
+    x[j + 1] = j0 + j + 1 <= last ? e1 * x[j + 1] : 0.0f;
   }
 }
 
@@ -355,9 +365,8 @@ template <int DK>
 __global__ void __launch_bounds__(kPrepThreads, 4)
     prepare_kernel(const Args a) {
   using P = PrepCfg<DK>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_la[];
+  uint8_t* const smem = smem_la;
   float* const L = reinterpret_cast<float*>(smem + P::L_OFF);
   float* const T = reinterpret_cast<float*>(smem + P::T_OFF);
   float* const M = reinterpret_cast<float*>(smem + P::M_OFF);
@@ -372,7 +381,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   const int slot = blockIdx.x / a.h_v;
   if (t == 0) {
     ptx::mbar_init(bar, 1);
-    *abort_flag = 0u;
+    // the swizzled images need the alignment that the declaration asks for
+    *abort_flag = (ptx::smem_u32(smem) & 1023u) != 0u ? 1u : 0u;
+    if (*abort_flag) atomicOr(&g_fault_word, kFaultPrepare);
     ptx::fence_mbarrier_init();
   }
   if (warp == 1) {
@@ -413,19 +424,20 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     const float* g = a.decay + tok0 * a.h_v + h;
     if (2 * lane < len) x0 = g[static_cast<int64_t>(2 * lane) * a.h_v];
     if (2 * lane + 1 < len) x1 = g[static_cast<int64_t>(2 * lane + 1) * a.h_v];
-  } else if (warp >= 2 && t - 64 < len) {
+  } else if (t >= 64 && t < 128 && t - 64 < len) {
     bt = a.beta != nullptr ? a.beta[(tok0 + t - 64) * a.h_v + h] : 1.0f;
   }
   // [K; Q] -> the swizzled image, rows past the sequence zero; the group's
   // first head also writes it out
   {
-    constexpr int kUnits = DK / 8;  // 16-byte units per row, and per thread
+    constexpr int kUnits = DK / 8;            // 16-byte units per row
+    constexpr int kStep = kPrepThreads / kUnits;  // rows per pass
     uint8_t* const image = a.kq + (static_cast<int64_t>(slot) * a.h_k + hk) * P::KQ;
     const int u = t % kUnits;
-    uint4 x[kUnits];
+    uint4 x[128 / kStep];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int r = t / kUnits + i * (kPrepThreads / kUnits), tok = r & (C - 1);
+    for (int i = 0; i < 128 / kStep; ++i) {
+      const int r = t / kUnits + i * kStep, tok = r & (C - 1);
       x[i] = make_uint4(0u, 0u, 0u, 0u);
       if (tok < len) {
         const __nv_bfloat16* row = r < C ? a.k + (tok0 + tok) * a.ldk : a.q + (tok0 + tok) * a.ldq;
@@ -433,8 +445,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       }
     }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int r = t / kUnits + i * (kPrepThreads / kUnits);
+    for (int i = 0; i < 128 / kStep; ++i) {
+      const int r = t / kUnits + i * kStep;
       const uint32_t off = (u / 8) * kHalfBytes + sw128(r, u % 8);
       *reinterpret_cast<uint4*>(smem + off) = x[i];
       if (h % group == 0) *reinterpret_cast<uint4*>(image + off) = x[i];
@@ -455,7 +467,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     const float h0 = static_cast<float>(s0), h1 = static_cast<float>(s);
     G[2 * lane] = make_float2(h0, static_cast<float>(s0 - h0));
     G[2 * lane + 1] = make_float2(h1, static_cast<float>(s - h1));
-  } else if (warp >= 2) {
+  } else if (t >= 64 && t < 128) {
     Beta[t - 64] = bt;
   }
   ptx::fence_proxy_async_smem();
@@ -464,7 +476,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t sb = ptx::smem_u32(smem);
-  if (t == 0) {
+  bool ok = *abort_flag == 0u;
+  if (t == 0 && ok) {
     // [K; Q] K^T: 128 x 64
     constexpr uint32_t kScores = ptx::idesc_bf16(128, C, false, false);
 #pragma unroll
@@ -474,51 +487,54 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     }
     ptx::tc_commit(bar);
   }
-  bool ok = warp_wait(bar, 0, abort_flag, kFaultPrepare);
+  ok = ok && warp_wait(bar, 0, abort_flag, kFaultPrepare);
   ptx::tc_fence_after();
   __syncthreads();  // every warp saw the scores: L may go over their operands
-  const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-  const int row = t & (C - 1);
+  // this thread: row r of the 128 (a token's row of L and T, then of A and AT),
+  // columns [j0, j0 + 32)
+  const int r = (warp & 3) * 32 + lane, row = r & (C - 1), j0 = 32 * (warp >> 2);
+  const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j0;
   const bool delta = a.beta != nullptr;
   uint8_t* const out = a.tt + (static_cast<int64_t>(slot) * a.h_v + h) * kHeadBytes;
-  float x[C];
+  float x[32];
   tc_ld(lanes, x);
-  if (t < C) {
-    const float2 gt = G[row], ge = G[C - 1];
+  if (r < C) {
     const float f = Beta[row];
-    float* gate = reinterpret_cast<float*>(out + 2 * kTTBytes);
-    gate[row] = ptx::ex2(gt.x + gt.y);
-    gate[C + row] = ptx::ex2((ge.x - gt.x) + (ge.y - gt.y));
-    gate[2 * C + row] = f;
-    if (row == 0) gate[3 * C] = ptx::ex2(ge.x + ge.y);
+    if (j0 == 0) {
+      const float2 gt = G[row], ge = G[C - 1];
+      float* gate = reinterpret_cast<float*>(out + 2 * kTTBytes);
+      gate[row] = ptx::ex2(gt.x + gt.y);
+      gate[C + row] = ptx::ex2((ge.x - gt.x) + (ge.y - gt.y));
+      gate[2 * C + row] = f;
+      if (row == 0) gate[3 * C] = ptx::ex2(ge.x + ge.y);
+    }
     if (delta) {
-      decay_row(x, G, row, row - 1, f);
+      decay_row(x, G, row, j0, row - 1, f);
 #pragma unroll
-      for (int j = 0; j < C; j += 4) {
-        *reinterpret_cast<float4*>(L + row * kLd + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-        if (j >= (row & ~15) + 16)
-          *reinterpret_cast<float4*>(T + row * kLd + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(L + row * kLd + j0 + j) =
+            make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
     } else {
       // without the delta rule T = I, and A itself stands in the place of AT
 #pragma unroll
-      for (int j = 0; j < C; ++j) x[j] = j == row ? 1.0f : 0.0f;
+      for (int j = 0; j < 32; ++j) x[j] = j0 + j == row ? 1.0f : 0.0f;
     }
   } else {
-    decay_row(x, G, row, row, 1.0f);
-    if (delta) store_image_row(sb + P::A_OFF, P::A_PIECE, row, x);  // 64 rows from a multiple of 8
+    decay_row(x, G, row, j0, row, 1.0f);
+    if (delta) store_image_row(sb + P::A_OFF, P::A_PIECE, row, j0 / 8, x);  // rows from a multiple of 8
   }
   if (delta) {
     __syncthreads();
     invert_unit_lower(L, T, M, t);
-    if (t < C) {
+    if (r < C) {
 #pragma unroll
-      for (int j = 0; j < C; j += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(T + row * kLd + j);
+      for (int j = 0; j < 32; j += 4) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (j0 + j <= (row | 15)) v = *reinterpret_cast<const float4*>(T + row * kLd + j0 + j);
         x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
       }
       // over L, which the inverse no longer needs
-      store_row_split<2>(sb + P::L_OFF, 8192, row, 1024, x);
+      store_row_split<2>(sb + P::L_OFF + (j0 / 8) * 1024, 8192, row, 1024, x);
     }
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
@@ -541,20 +557,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     }
     ok = ok && warp_wait(bar, 1, abort_flag, kFaultPrepare);
     ptx::tc_fence_after();
-    if (t >= C) {
+    if (r >= C) {
       float y[32];
       tc_ld(lanes, x);
+      tc_ld(lanes + C, y);
 #pragma unroll
-      for (int c = 0; c < C; c += 32) {
-        tc_ld(lanes + C + c, y);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[c + j] += y[j];
-      }
+      for (int j = 0; j < 32; ++j) x[j] += y[j];
     }
     __syncthreads();  // every warp saw the product done: the image may go over T's pieces
   }
   // hi image at T_OFF, lo image at L_OFF
-  store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, t, x);
+  store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, r, j0 / 8, x);
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();
@@ -625,8 +638,8 @@ template <int DK>
 __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
     chain_kernel(const Args a) {
   using P = ChainCfg<DK>;
-  extern __shared__ __align__(1024) uint8_t smem_chain[];
-  uint8_t* const smem = smem_chain;
+  extern __shared__ __align__(1024) uint8_t smem_la[];
+  uint8_t* const smem = smem_la;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);  // [2] K; Q loaded
   uint64_t* const s_ready = full + 2;   // operand pieces written by the compute warps
   uint64_t* const x_ready = full + 3;

@@ -15,6 +15,11 @@ after the gates:
 did not survive extraction, and this is the Gated DeltaNet form the abstract's
 wording describes). Errors are relative Frobenius norms over tokens x heads.
 
+What the gates' errors do to the layer is measured too: the gated delta rule
+(nvfp4_linear_attention) runs over the same tokens as one prompt, with synthetic
+unit keys and queries, once with the exact gates and once with the quantized
+ones, and the outputs (``out``) and final states (``state``) are compared.
+
     python -m nvfp4_w4a4_quantized_elem_b200.gate_sensitivity [--rows N]
 """
 from __future__ import annotations
@@ -38,6 +43,14 @@ def _gates(y_a, y_b, a_log, dt_bias):
     return g, torch.exp(g), torch.sigmoid(y_b)
 
 
+def _recurrence(qkv, g, beta):
+    """Outputs and final state of the layer's recurrence over one prompt."""
+    q, k, v = qkv
+    state = torch.empty((1, v.shape[1], k.shape[2], v.shape[2]), device=q.device)
+    o = nvfp4.linear_attention(q, k, v, g.float(), beta.float(), state=state)
+    return o.double(), state.double()
+
+
 def _rel(a: torch.Tensor, b: torch.Tensor) -> float:
     return float(torch.linalg.norm(a - b) / torch.linalg.norm(b))
 
@@ -52,6 +65,7 @@ def measure(rows: int = 8192, sigmas_a=SIGMAS_A, device="cuda") -> list[dict]:
     Wb = nvfp4.quantize(w_b)
     xd = x.double()
     y_b_ref = xd @ w_b.double().T
+    qkv = [t.to(device) for t in cfg.qkv(rows)]
     out = []
     for sa in sigmas_a:
         w_a = cfg.w_a(sa).to(device)
@@ -61,10 +75,13 @@ def measure(rows: int = 8192, sigmas_a=SIGMAS_A, device="cuda") -> list[dict]:
         h = cfg.heads
         g0, al0, be0 = _gates(y_a_ref, y_b_ref, a_log, dt_bias)
         g1, al1, be1 = _gates(y[:, :h], y[:, h:], a_log, dt_bias)
+        o0, s0 = _recurrence(qkv, g0, be0)
+        o1, s1 = _recurrence(qkv, g1, be1)
         out.append({"sigma_a": sa, "rows": rows,
                     "preact_a_std": float(y_a_ref.std()), "preact_b_std": float(y_b_ref.std()),
                     "gemm_a": _rel(y[:, :h], y_a_ref), "gemm_b": _rel(y[:, h:], y_b_ref),
-                    "g": _rel(g1, g0), "alpha": _rel(al1, al0), "beta": _rel(be1, be0)})
+                    "g": _rel(g1, g0), "alpha": _rel(al1, al0), "beta": _rel(be1, be0),
+                    "out": _rel(o1, o0), "state": _rel(s1, s0)})
     return out
 
 

@@ -175,6 +175,15 @@ class Gates:
     def w_b(self) -> torch.Tensor:
         return gaussian_bf16(self.heads, self.k, 0.005, 4)
 
+    def qkv(self, rows: int | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """Queries and keys [m, 16, 128], unit length (GDN's L2-normed q / k; three
+        value heads per key head), and values [m, heads, 128] ~N(0,1); seeds 7-9."""
+        m, d, hk = rows or self.m, 128, self.heads // 3
+        unit = lambda t: torch.nn.functional.normalize(t.float(), dim=-1).to(torch.bfloat16)
+        return (unit(gaussian_bf16(m, hk * d, 1.0, 7).view(m, hk, d)),
+                unit(gaussian_bf16(m, hk * d, 1.0, 8).view(m, hk, d)),
+                gaussian_bf16(m, self.heads * d, 1.0, 9).view(m, self.heads, d))
+
     def a_log(self) -> torch.Tensor:
         g = torch.Generator().manual_seed(5)
         return torch.log(1.0 + 15.0 * torch.rand(self.heads, generator=g, dtype=torch.float64))

@@ -182,14 +182,13 @@ __device__ __forceinline__ void tc_ld(uint32_t taddr, float (&x)[N]) {
   ptx::tc_wait_ld();
 }
 
-// Bounded wait (2 s): many tries between two looks at the clock, since the
-// waits of the chain are short and stand one behind the other.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
-                                             volatile uint32_t* abort_flag, uint32_t who) {
-  for (int i = 0; i < 64; ++i)
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+// The slow part of a wait, out of line: many tries between two looks at the
+// clock, at most 2 s.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity,
+                                       volatile uint32_t* abort_flag, uint32_t who) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (true) {
+#pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (ptx::mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
@@ -199,6 +198,13 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
       return false;
     }
   }
+}
+
+// Bounded wait: one try in line, the rest out of line (the waits of the chain
+// are short and stand one behind the other).
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
+                                             volatile uint32_t* abort_flag, uint32_t who) {
+  return ptx::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, who);
 }
 
 // Used only while aborting: wait for in-flight asynchronous work, bounded.

@@ -15,10 +15,13 @@
 //   u = beta (v - e^g p),  o = scale (e^g r + (q.k) u),  S <- e^g S + k u^T
 // one pass over the registers gives both sums, with one reduction between the
 // threads, and S goes from memory to registers and back without shared memory.
-// A CTA owns 32 of the d_v columns of one (token, head): 128 threads as 16
-// row groups x 8 lanes of float4 columns, so a warp's load is four whole 128-byte
-// lines, a thread has d_k / 16 loads in flight, and one token of 32 heads
-// already gives 128 CTAs.
+// A CTA of 128 threads owns COLS of the d_v columns of one (token, head): row
+// groups of COLS / 4 lanes with a float4 of columns each, whole 128-byte lines
+// per row, 8 rows a thread. COLS = 32 for d_k = 128 (one token of 32 heads
+// already gives 128 CTAs), 64 for d_k = 64 where d_v allows: with 4 rows a thread
+// there were too few bytes in flight (256 rows of 24 heads 76 -> 66 us). 64
+// registers, so that 8 CTAs share an SM (96 left to the compiler, 5 CTAs: 256
+// rows of 32 heads x 128 x 128 took 199 us instead of 162, 5.8 TB/s).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,7 +33,11 @@ namespace nvfp4 {
 namespace la {
 
 constexpr int kStepThreads = 128;
-constexpr int kStepCols = 32;   // d_v columns per CTA
+
+// d_v columns per CTA
+__host__ __device__ constexpr int step_cols(int d_k, int d_v) {
+  return d_k == 64 && d_v % 64 == 0 ? 64 : 32;
+}
 
 struct StepArgs {
   const __nv_bfloat16* q;   // [batch][ldq], head h at h * d_k
@@ -50,20 +57,22 @@ struct StepArgs {
 // Tokens that name the same slot are taken in order by the CTAs of the first
 // of them, with the state kept in registers between them; a token whose slot
 // lies outside the pool is padding, its row of o stays as it was.
-template <int DK>
-__global__ void __launch_bounds__(kStepThreads)
+template <int DK, int COLS>
+__global__ void __launch_bounds__(kStepThreads, 8)
     step_kernel(const StepArgs a) {
-  constexpr int R = DK / 16;   // rows per thread
+  constexpr int LANES = COLS / 4;                // lanes of a row
+  constexpr int GROUPS = kStepThreads / LANES;   // rows at a time
+  constexpr int R = DK / GROUPS;                 // rows per thread
   __shared__ float s_q[DK], s_k[DK];
-  __shared__ float4 s_red[2][4][8];
+  __shared__ float4 s_red[2][4][LANES];
   __shared__ float s_qk[4];
   __shared__ int s_next;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int col = (t & 7) * 4, row0 = t >> 3;   // this thread's columns, first row
-  const int blocks = a.d_v / kStepCols;
+  const int col = (t % LANES) * 4, row0 = t / LANES;   // this thread's columns, first row
+  const int blocks = a.d_v / COLS;
   const int h = (blockIdx.x / blocks) % a.h_v;
   int b = blockIdx.x / blocks / a.h_v;
-  const int c0 = (blockIdx.x % blocks) * kStepCols;
+  const int c0 = (blockIdx.x % blocks) * COLS;
   const int hk = h / (a.h_v / a.h_k);
   ptx::grid_dep_launch();
   ptx::grid_dep_wait();
@@ -73,7 +82,7 @@ __global__ void __launch_bounds__(kStepThreads)
   float4 s[R];
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    s[i] = __ldcs(reinterpret_cast<const float4*>(S + static_cast<int64_t>(row0 + 16 * i) * a.d_v));
+    s[i] = __ldcs(reinterpret_cast<const float4*>(S + static_cast<int64_t>(row0 + GROUPS * i) * a.d_v));
   while (true) {
     // the next token of this slot; an earlier one means other CTAs own it
     int next = a.batch;
@@ -110,18 +119,18 @@ __global__ void __launch_bounds__(kStepThreads)
     float4 p = make_float4(0, 0, 0, 0), r = p;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const float ki = s_k[row0 + 16 * i], qi = s_q[row0 + 16 * i];
+      const float ki = s_k[row0 + GROUPS * i], qi = s_q[row0 + GROUPS * i];
       p.x += ki * s[i].x; p.y += ki * s[i].y; p.z += ki * s[i].z; p.w += ki * s[i].w;
       r.x += qi * s[i].x; r.y += qi * s[i].y; r.z += qi * s[i].z; r.w += qi * s[i].w;
     }
 #pragma unroll
-    for (int d = 8; d <= 16; d <<= 1) {
+    for (int d = LANES; d <= 16; d <<= 1) {
       p.x += __shfl_xor_sync(0xFFFFFFFFu, p.x, d); p.y += __shfl_xor_sync(0xFFFFFFFFu, p.y, d);
       p.z += __shfl_xor_sync(0xFFFFFFFFu, p.z, d); p.w += __shfl_xor_sync(0xFFFFFFFFu, p.w, d);
       r.x += __shfl_xor_sync(0xFFFFFFFFu, r.x, d); r.y += __shfl_xor_sync(0xFFFFFFFFu, r.y, d);
       r.z += __shfl_xor_sync(0xFFFFFFFFu, r.z, d); r.w += __shfl_xor_sync(0xFFFFFFFFu, r.w, d);
     }
-    if (lane < 8) {
+    if (lane < LANES) {
       s_red[0][warp][lane] = p;
       s_red[1][warp][lane] = r;
     }
@@ -129,7 +138,7 @@ __global__ void __launch_bounds__(kStepThreads)
     float pj[4] = {0, 0, 0, 0}, rj[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float4 x = s_red[0][w][t & 7], y = s_red[1][w][t & 7];
+      const float4 x = s_red[0][w][t % LANES], y = s_red[1][w][t % LANES];
       pj[0] += x.x; pj[1] += x.y; pj[2] += x.z; pj[3] += x.w;
       rj[0] += y.x; rj[1] += y.y; rj[2] += y.z; rj[3] += y.w;
     }
@@ -143,7 +152,7 @@ __global__ void __launch_bounds__(kStepThreads)
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const float ki = s_k[row0 + 16 * i];
+      const float ki = s_k[row0 + GROUPS * i];
       s[i].x = e * s[i].x + ki * u[0]; s[i].y = e * s[i].y + ki * u[1];
       s[i].z = e * s[i].z + ki * u[2]; s[i].w = e * s[i].w + ki * u[3];
     }
@@ -158,7 +167,7 @@ __global__ void __launch_bounds__(kStepThreads)
   }
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    __stcs(reinterpret_cast<float4*>(S + static_cast<int64_t>(row0 + 16 * i) * a.d_v), s[i]);
+    __stcs(reinterpret_cast<float4*>(S + static_cast<int64_t>(row0 + GROUPS * i) * a.d_v), s[i]);
 }
 
 }  // namespace la

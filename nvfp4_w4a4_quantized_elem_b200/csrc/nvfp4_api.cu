@@ -1344,7 +1344,8 @@ nvfp4_status nvfp4_linear_attention_step(const void* q, int64_t ldq, const void*
                                    state, n_slots, slots, o, ldo))
     return e;
   if (state == nullptr || (slots == nullptr && n_slots < batch)) return NVFP4_ERR_INVALID_ARG;
-  const int64_t grid = batch * h_v * (d_v / kStepCols);
+  const int cols = step_cols(d_k, d_v);
+  const int64_t grid = batch * h_v * (d_v / cols);
   if (grid >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
   if (batch == 0) return NVFP4_OK;
   StepArgs a;
@@ -1367,8 +1368,9 @@ nvfp4_status nvfp4_linear_attention_step(const void* q, int64_t ldq, const void*
   a.n_slots = static_cast<int>(n_slots);
   a.slots = slots;
   a.o = static_cast<__nv_bfloat16*>(o);
-  return launch_pdl(d_k == 128 ? step_kernel<128> : step_kernel<64>, static_cast<unsigned>(grid),
-                    kStepThreads, 0, reinterpret_cast<cudaStream_t>(stream), 1u, a);
+  const auto kernel = d_k == 128 ? step_kernel<128, 32>
+                      : cols == 64 ? step_kernel<64, 64> : step_kernel<64, 32>;
+  return launch_pdl(kernel, static_cast<unsigned>(grid), kStepThreads, 0, reinterpret_cast<cudaStream_t>(stream), 1u, a);
 }
 
 nvfp4_status nvfp4_silu_mul(const void* y, int64_t m, int64_t n, int64_t ldy, void* h,

@@ -396,6 +396,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     ptx::tmem_alloc(tmem_holder, 128);
     ptx::tmem_relinquish();
   }
+  // The chain's CTAs may start only when every CTA here has its tensor memory:
+  // they take theirs and wait for this grid.
+  __syncthreads();
   ptx::grid_dep_launch();
   ptx::grid_dep_wait();
   // the last sequence whose first slot is at or below this one: the slots of
@@ -581,7 +584,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     ptx::bulk_store(out, smem + P::T_OFF, kTTBytes);
     ptx::bulk_store(out + kTTBytes, smem + P::L_OFF, kTTBytes);
     ptx::bulk_commit_group();
-    ptx::bulk_wait_group_read<0>();
+    ptx::bulk_wait_group_all();
   }
   ptx::tc_fence_after();
   if (warp == 1) {

@@ -119,6 +119,16 @@ def test_head_layouts(nv, hk, hv, dk, dv, delta, resume):
     run_prompts(nv, [130, 7], hk, hv, dk, dv, delta, resume, hk + hv + dv)
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 256)])
+@pytest.mark.parametrize("delta", [True, False])
+@pytest.mark.parametrize("strong", [True, False])
+def test_many_sequences(nv, dk, dv, delta, strong):
+    """More CTAs of the chain than the GPU holds at a time, lengths around whole
+    chunks."""
+    lens = [1, 64, 65, 200, 63, 0, 128, 129, 2, 70] * 4
+    run_prompts(nv, lens, 2, 4, dk, dv, delta, True, 31 + dv, strong=strong)
+
+
 @pytest.mark.parametrize("delta", [True, False])
 def test_strong_and_vanishing_decays(nv, delta):
     """Decays from e^-1000 to 1 next to one another in a chunk."""

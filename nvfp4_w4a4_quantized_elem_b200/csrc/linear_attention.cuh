@@ -606,6 +606,7 @@ constexpr int kCols = 16;                  // of them per compute thread
 // than pieces one after the other. Compute threads hold one row, 16 columns
 // wide (the splitting stands on the critical path: 32 columns a thread took 400
 // cycles more per operand); one more warp loads and issues the MMAs.
+// (The kernel of the delta rule; the plain one is below.)
 // A step of one chunk is a chain of latencies (4.4 K cycles, 1.2 K of them in
 // MMAs), so two CTAs share an SM and fill each other's gaps; for that the
 // shared memory is cut to half an SM's: S, X and U~ take turns in one region,
@@ -628,6 +629,53 @@ struct ChainCfg {
   static constexpr uint32_t TMEM = 256;
   static_assert(2 * (SMEM + 1024) <= 228 * 1024 && 2 * D2_COL <= TMEM, "two CTAs per SM");
 };
+
+// The pool slot of sequence b, or -1: only the first sequence that names a slot
+// has it. Called by whole warps.
+__device__ __forceinline__ int state_slot(const Args& a, int b, int lane) {
+  if (a.state == nullptr) return -1;
+  const int slot = a.slots != nullptr ? a.slots[b] : b;
+  if (slot < 0 || slot >= a.n_slots) return -1;
+  int earlier = 0;
+  if (a.slots != nullptr)
+    for (int i = lane; i < b; i += 32) earlier |= a.slots[i] == slot;
+  return __any_sync(0xFFFFFFFFu, earlier) ? -1 : slot;
+}
+
+// 16 columns of a state row, zero unless the sequence resumes.
+__device__ __forceinline__ void load_state(const Args& a, bool has, int b, const float* row,
+                                           float (&S)[kCols]) {
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) S[j] = 0.0f;
+  if (has && a.resume != nullptr && a.resume[b] != 0) {
+#pragma unroll
+    for (int j = 0; j < kCols / 4; ++j) {
+      const float4 x = reinterpret_cast<const float4*>(row)[j];
+      S[4 * j] = x.x; S[4 * j + 1] = x.y; S[4 * j + 2] = x.z; S[4 * j + 3] = x.w;
+    }
+  }
+}
+
+__device__ __forceinline__ void store_state(float* row, const float (&S)[kCols]) {
+#pragma unroll
+  for (int j = 0; j < kCols / 4; ++j)
+    reinterpret_cast<float4*>(row)[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+}
+
+// o = scale (e^G (Q S) + A U), 16 columns of one token.
+__device__ __forceinline__ void store_out(__nv_bfloat16* o, float scale, float eg,
+                                          const float (&qs)[kCols], const float (&au)[kCols]) {
+#pragma unroll
+  for (int u = 0; u < kCols / 8; ++u) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = 8 * u + 2 * e;
+      w[e] = round_piece(scale * (eg * qs[j] + au[j]), scale * (eg * qs[j + 1] + au[j + 1]));
+    }
+    *reinterpret_cast<uint4*>(o + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
 
 // This thread's 16 columns of the BLOCKS column blocks of a result, added.
 template <int BLOCKS>
@@ -782,30 +830,12 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
     const bool is_k = (warp & 3) < 2;           // rows of K and U; else rows of Q and O
     const int cols = (warp >> 2) * kCols;       // this thread's columns of the block
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + cols;
-    int slot = -1;
-    if (a.state != nullptr) {
-      slot = a.slots != nullptr ? a.slots[b] : b;
-      if (slot < 0 || slot >= a.n_slots) slot = -1;
-      if (slot >= 0 && a.slots != nullptr) {  // only the first sequence that names a slot has it
-        int earlier = 0;
-        for (int i = lane; i < b; i += 32) earlier |= a.slots[i] == slot;
-        if (__any_sync(0xFFFFFFFFu, earlier)) slot = -1;
-      }
-    }
+    const int slot = state_slot(a, b, lane);
     const int64_t col = static_cast<int64_t>(h) * a.d_v + c0 + cols;  // column of V and O
-    float* const state = a.state + (static_cast<int64_t>(slot) * a.h_v * DK + k_row) * a.d_v +
-                         static_cast<int64_t>(h) * DK * a.d_v + c0 + cols;
+    float* const state = a.state + ((static_cast<int64_t>(slot) * a.h_v + h) * DK + k_row) * a.d_v +
+                         c0 + cols;
     float S[kCols];
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) S[j] = 0.0f;
-    if (slot >= 0 && k_row < DK && a.resume != nullptr && a.resume[b] != 0) {
-#pragma unroll
-      for (int j = 0; j < kCols / 4; ++j) {
-        const float4 x = reinterpret_cast<const float4*>(state)[j];
-        S[4 * j] = x.x; S[4 * j + 1] = x.y; S[4 * j + 2] = x.z; S[4 * j + 3] = x.w;
-      }
-    }
-    const bool delta = a.beta != nullptr;
+    load_state(a, slot >= 0 && k_row < DK, b, state, S);
     // what the next chunk needs from memory, requested a chunk ahead
     float eg = 0.0f, erest = 0.0f, bt = 0.0f, eall = 0.0f;
     uint4 v[kCols / 8];
@@ -854,8 +884,8 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
           for (int e = 0; e < 4; ++e) {
             const int j = 8 * u + 2 * e;
             const float v0 = __uint_as_float(w[e] << 16), v1 = __uint_as_float(w[e] & 0xFFFF0000u);
-            D[j] = delta ? bt * (v0 - eg_c * Q[j]) : v0;
-            D[j + 1] = delta ? bt * (v1 - eg_c * Q[j + 1]) : v1;
+            D[j] = bt * (v0 - eg_c * Q[j]);
+            D[j + 1] = bt * (v1 - eg_c * Q[j + 1]);
           }
         }
         store_row_split<kPieces>(r_x, P::X_PIECE, row, C * 16, D);
@@ -873,17 +903,7 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
         store_row_split<kPieces>(r_x, P::X_PIECE, row, C * 16, D);
         publish(u_ready);
       } else if (tok < end) {
-        __nv_bfloat16* o = a.o + tok * a.ldo + col;
-#pragma unroll
-        for (int u = 0; u < kCols / 8; ++u) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = 8 * u + 2 * e;
-            w[e] = round_piece(a.scale * (eg_c * Q[j] + D[j]), a.scale * (eg_c * Q[j + 1] + D[j + 1]));
-          }
-          *reinterpret_cast<uint4*>(o + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        store_out(a.o + tok * a.ldo + col, a.scale, eg_c, Q, D);
       }
       if (!(ok = warp_wait(d3, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
@@ -891,12 +911,260 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
 #pragma unroll
       for (int j = 0; j < kCols; ++j) S[j] = eall_c * S[j] + D[j];
     }
-    if (ok && slot >= 0 && k_row < DK) {
+    if (ok && slot >= 0 && k_row < DK) store_state(state, S);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    ptx::tmem_dealloc(tmem, P::TMEM);
+  }
+}
+
+// ------------------------------------------------- chain without the delta rule --
+
+// Without the delta rule U = V, and of a chunk's products only Q S waits for the
+// state: A V and K^T U~, U~ = diag(e^{G_64-G}) V, need V alone, and the state's
+// own chain is S' = e^{G_64} S + K^T U~ in registers. So A V and K^T U~ of a chunk
+// run while its state is cut into pieces and the chunk before is written out,
+// and a step takes one product's latency instead of three. V enters in one
+// piece (exact). Of the [I; A] image only the rows of A are loaded: the product's
+// rows 0..63, which would be V itself, come from whatever stands before them in
+// shared memory and are not read. The rest is chain_kernel's.
+template <int DK>
+struct PlainCfg {
+  static constexpr int WARPS = 4 * (DVB / kCols);
+  static constexpr int THREADS = 32 * WARPS + 32;
+  static constexpr int S_PIECE = DK * DVB * 2;
+  static constexpr int X_PIECE = C * DVB * 2;
+  static constexpr int A_BYTES = kTTBytes / 2;       // one piece of A
+  static constexpr int A_OFF = 2 * kq_bytes(DK);     // [2][2] pieces
+  static constexpr int S_OFF = A_OFF + 4 * A_BYTES;
+  static constexpr int V_OFF = S_OFF + kSPieces * S_PIECE;
+  static constexpr int U_OFF = V_OFF + X_PIECE;
+  static constexpr int BAR_OFF = U_OFF + kPieces * X_PIECE;
+  static constexpr int SMEM = BAR_OFF + 128;   // the base is 1024-byte aligned
+  static constexpr int PER_SM = DK == 64 ? 2 : 1;
+  // tensor memory: Q S (with K S), A V (with I V), K^T U~
+  static constexpr uint32_t D1 = 0, D2 = kSPieces * DVB, D3 = D2 + DVB;
+  static constexpr uint32_t TMEM = 256;
+  static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024 && SMEM <= 227 * 1024 &&
+                    D3 + kPieces * DVB <= TMEM, "CTAs per SM");
+};
+
+template <int DK>
+__global__ void __launch_bounds__(PlainCfg<DK>::THREADS, PlainCfg<DK>::PER_SM)
+    plain_kernel(const Args a) {
+  using P = PlainCfg<DK>;
+  extern __shared__ __align__(1024) uint8_t smem_la[];
+  uint8_t* const smem = smem_la;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);  // [2] K; Q and A loaded
+  uint64_t* const v_ready = full + 2;   // V and U~ written, A V and K^T U~ before them taken
+  uint64_t* const s_ready = full + 3;   // S written, Q S before it taken
+  uint64_t* const d1 = full + 4;        // Q S complete
+  uint64_t* const d23 = full + 5;       // A V and K^T U~ complete
+  uint64_t* const drain = full + 6;
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(full + 7);
+  volatile uint32_t* const abort_flag = tmem_holder + 1;
+
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int blocks = a.d_v / DVB;
+  const int c0 = (blockIdx.x % blocks) * DVB;
+  const int h = (blockIdx.x / blocks) % a.h_v;
+  const int b = blockIdx.x / blocks / a.h_v;
+  const int hk = h / (a.h_v / a.h_k);
+  constexpr int kMmaWarp = P::WARPS;
+  if (t == 0) {
+    ptx::mbar_init(&full[0], 1);
+    ptx::mbar_init(&full[1], 1);
+    ptx::mbar_init(v_ready, P::WARPS);
+    ptx::mbar_init(s_ready, P::WARPS);
+    ptx::mbar_init(d1, 1);
+    ptx::mbar_init(d23, 1);
+    ptx::mbar_init(drain, 1);
+    // the swizzled images need the alignment that the declaration asks for
+    *abort_flag = (ptx::smem_u32(smem) & 1023u) != 0u ? 1u : 0u;
+    if (*abort_flag) atomicOr(&g_fault_word, kFaultChain);
+    ptx::fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(tmem_holder, P::TMEM);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  ptx::grid_dep_launch();
+  ptx::grid_dep_wait();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t sb = ptx::smem_u32(smem);
+  int start, end;
+  seq_range(a, b, start, end);
+  const int n = (end - start + C - 1) / C;
+  const int slot0 = first_slot(start, b);
+
+  // every barrier's phase c is chunk c's
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      auto load = [&](int c) {
+        uint64_t* bar = &full[c & 1];
+        uint8_t* const pieces = smem + P::A_OFF + (c & 1) * 2 * P::A_BYTES;
+        const uint8_t* const image =
+            a.tt + ((static_cast<int64_t>(slot0) + c) * a.h_v + h) * kHeadBytes + P::A_BYTES;
+        ptx::mbar_arrive_expect_tx(bar, kq_bytes(DK) + 2 * P::A_BYTES);
+        ptx::bulk_load(smem + (c & 1) * kq_bytes(DK),
+                       a.kq + ((static_cast<int64_t>(slot0) + c) * a.h_k + hk) * kq_bytes(DK),
+                       kq_bytes(DK), bar);
+        ptx::bulk_load(pieces, image, P::A_BYTES, bar);
+        ptx::bulk_load(pieces + P::A_BYTES, image + kTTBytes, P::A_BYTES, bar);
+      };
+      constexpr uint32_t kI1 = ptx::idesc_bf16(128, kSPieces * DVB, false, true);
+      constexpr uint32_t kI2 = ptx::idesc_bf16(128, DVB, false, true);
+      constexpr uint32_t kI3 = ptx::idesc_bf16(128, kPieces * DVB, true, true);
+      constexpr uint32_t kSN = DK * 16, kXN = C * 16;  // bytes between groups of 8 columns
+      int asked = 0, arrived = 0;  // chunks
+      bool ok = *abort_flag == 0u;
+      if (n > 0 && ok) load(asked++);
+      for (int c = 0; c < n && ok; ++c) {
+        const uint32_t par = c & 1;
+        const uint32_t kq = sb + par * kq_bytes(DK);
+        const uint32_t pieces = sb + P::A_OFF + par * 2 * P::A_BYTES;
+        ok = wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma);
+        if (!ok) break;
+        ++arrived;
+        ok = wait_bounded(v_ready, par, abort_flag, kFaultChainMma);
+        if (!ok) break;
+        ptx::tc_fence_after();
 #pragma unroll
-      for (int j = 0; j < kCols / 4; ++j)
-        reinterpret_cast<float4*>(state)[j] =
-            make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+        for (int s = 0; s < C / 16; ++s)   // K^T U~ (64 of d_k: the upper rows repeat the lower)
+          ptx::tc_mma_bf16(tmem + P::D3,
+                           ptx::smem_desc(kq + s * 2048, DK == 128 ? kHalfBytes : 0, 1024, 2),
+                           ptx::smem_desc(sb + P::U_OFF + s * 256, 128, kXN, 0), kI3, s != 0);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)        // [*; A] V, A in two pieces
+#pragma unroll
+          for (int s = 0; s < C / 16; ++s)
+            ptx::tc_mma_bf16(tmem + P::D2,
+                             ptx::smem_desc(pieces + (p - 1) * P::A_BYTES + s * 32, 16, 1024, 2),
+                             ptx::smem_desc(sb + P::V_OFF + s * 256, 128, kXN, 0), kI2, (p | s) != 0);
+        ptx::tc_commit(d23);
+        ok = wait_bounded(s_ready, par, abort_flag, kFaultChainMma);
+        if (!ok) break;
+        // S in place: Q S of the chunk before is taken, and with it the last
+        // reader of the other buffers complete
+        if (c + 1 < n) load(asked++);
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int s = 0; s < DK / 16; ++s)   // [K; Q] S
+          ptx::tc_mma_bf16(tmem + P::D1, ptx::smem_desc(kq + (s / 4) * kHalfBytes + (s % 4) * 32, 16, 1024, 2),
+                           ptx::smem_desc(sb + P::S_OFF + s * 256, 128, kSN, 0), kI1, s != 0);
+        ptx::tc_commit(d1);
+      }
+      if (!ok) {  // let what is in flight end before the CTA does
+        ptx::tc_commit(drain);
+        drain_wait(drain, 0);
+        for (int c = arrived; c < asked; ++c) drain_wait(&full[c & 1], (c >> 1) & 1);
+      } else if (n > 0) {
+        drain_wait(d1, (n - 1) & 1);  // the last product, should the others give up on it
+      }
     }
+  } else {
+    const int k_row = (warp & 3) * 32 + lane;   // row of d_k
+    const int row = k_row & (C - 1);            // token of the chunk
+    const bool is_v = (warp & 3) < 2;           // rows of V and U~; else rows of Q and O
+    const int cols = (warp >> 2) * kCols;       // this thread's columns of the block
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + cols;
+    const int slot = state_slot(a, b, lane);
+    const int64_t col = static_cast<int64_t>(h) * a.d_v + c0 + cols;  // column of V and O
+    float* const state = a.state + ((static_cast<int64_t>(slot) * a.h_v + h) * DK + k_row) * a.d_v +
+                         c0 + cols;
+    float S[kCols];
+    load_state(a, slot >= 0 && k_row < DK, b, state, S);
+    // what the next chunk needs from memory, requested a chunk ahead
+    float gate = 0.0f, eall = 0.0f;   // e^{G_64 - G} of rows of V, e^G of rows of Q; e^{G_64}
+    uint4 v[kCols / 8];
+    auto fetch = [&](int c) {
+      const int64_t tok = start + static_cast<int64_t>(c) * C + row;
+      const float* g = reinterpret_cast<const float*>(
+          a.tt + ((static_cast<int64_t>(slot0) + c) * a.h_v + h) * kHeadBytes + 2 * kTTBytes);
+      gate = g[(is_v ? C : 0) + row];
+      eall = g[3 * C];
+#pragma unroll
+      for (int u = 0; u < kCols / 8; ++u) {
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (is_v && tok < end) v[u] = *reinterpret_cast<const uint4*>(a.v + tok * a.ldv + col + 8 * u);
+      }
+    };
+    auto arrive = [&](uint64_t* bar) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar);
+    };
+    auto publish = [&](uint64_t* bar) {  // operand rows written
+      ptx::fence_proxy_async_smem();
+      arrive(bar);
+    };
+    const uint32_t r_s = sb + P::S_OFF + (cols / 8) * (DK * 16);  // this thread's columns
+    const uint32_t r_v = sb + P::V_OFF + (cols / 8) * (C * 16);
+    const uint32_t r_u = sb + P::U_OFF + (cols / 8) * (C * 16);
+    bool ok = true;
+    float eg_before = 0.0f, eall_before = 0.0f;
+    if (n > 0) fetch(0);
+    // Chunk c begins where chunk c - 1 ends: its rows of the state and its
+    // outputs are taken from tensor memory here.
+    for (int c = 0; c <= n; ++c) {
+      const uint32_t par = c & 1, before = par ^ 1;
+      float D[kCols], AV[kCols];
+      if (c > 0) {
+        if (!(ok = warp_wait(d23, before, abort_flag, kFaultChain))) break;
+        ptx::tc_fence_after();
+        ld_sum<kPieces>(lanes + P::D3, D);
+        if (!is_v) {
+          ptx::tc_ld_32x32b_x16(lanes + P::D2, AV);
+          ptx::tc_wait_ld();
+        }
+      }
+      const float eg = gate, e_all = eall;
+      if (c < n) {
+        if (is_v) {
+          float u[kCols];
+#pragma unroll
+          for (int i = 0; i < kCols / 8; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            ptx::st_shared_v4(r_v + mn_off(row, i, C * 16), w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              u[8 * i + 2 * e] = eg * __uint_as_float(w[e] << 16);
+              u[8 * i + 2 * e + 1] = eg * __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+          }
+          store_row_split<kPieces>(r_u, P::X_PIECE, row, C * 16, u);
+          publish(v_ready);
+        } else {
+          arrive(v_ready);
+        }
+        if (c + 1 < n) fetch(c + 1);
+      }
+      if (c > 0) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) S[j] = eall_before * S[j] + D[j];
+        if (!(ok = warp_wait(d1, before, abort_flag, kFaultChain))) break;
+        ptx::tc_fence_after();
+      }
+      if (c > 0 && !is_v) ld_sum<kSPieces>(lanes + P::D1, D);  // Q S
+      if (c < n) {
+        if (DK == 128 || k_row < DK) store_row_split<kSPieces>(r_s, P::S_PIECE, k_row, DK * 16, S);
+        publish(s_ready);
+      }
+      if (c > 0 && !is_v) {
+        const int64_t tok = start + static_cast<int64_t>(c - 1) * C + row;
+        if (tok < end) store_out(a.o + tok * a.ldo + col, a.scale, eg_before, D, AV);
+      }
+      eg_before = eg;
+      eall_before = e_all;
+    }
+    if (ok && slot >= 0 && k_row < DK) store_state(state, S);
   }
   ptx::tc_fence_before();
   __syncthreads();

@@ -1248,23 +1248,27 @@ nvfp4_status la_smem(DeviceState* st, unsigned bit, K kernel, int bytes) {
 template <int DK>
 nvfp4_status launch_linear_attention(DeviceState* st, const nvfp4::la::Args& a, cudaStream_t s) {
   using namespace nvfp4::la;
-  using Chain = ChainCfg<DK>;
-  constexpr int kAloneSmem = 120 * 1024;
-  static_assert(Chain::SMEM <= kAloneSmem, "chain_kernel's shared memory");
-  const unsigned base = DK == 128 ? 0u : 2u;
+  const unsigned base = DK == 128 ? 0u : 3u;
   const int64_t prep = chunk_slots(a.total, a.n_seq) * a.h_v;
   const int64_t chain = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / DVB);
   if (prep >= (int64_t{1} << 31) || chain >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
   if (nvfp4_status e = la_smem(st, base, prepare_kernel<DK>, PrepCfg<DK>::SMEM)) return e;
-  if (nvfp4_status e = la_smem(st, base + 1, chain_kernel<DK>, kAloneSmem)) return e;
   if (nvfp4_status e = launch_pdl(prepare_kernel<DK>, static_cast<unsigned>(prep), kPrepThreads,
                                   PrepCfg<DK>::SMEM, s, 1u, a))
     return e;
+  const bool delta = a.beta != nullptr;
+  const auto kernel = delta ? chain_kernel<DK> : plain_kernel<DK>;
+  int smem = delta ? ChainCfg<DK>::SMEM : PlainCfg<DK>::SMEM;
   // At most one CTA per SM's worth: asking for more than half of an SM's shared
   // memory keeps them apart (they start while the first kernel's CTAs leave, and
   // two on one SM then took 8192 tokens of 32 heads from 447 to 561 us).
-  const int smem = chain <= st->sms ? kAloneSmem : Chain::SMEM;
-  return launch_pdl(chain_kernel<DK>, static_cast<unsigned>(chain), Chain::THREADS, smem, s, 1u, a);
+  constexpr int kAloneSmem = 130 * 1024;
+  static_assert(ChainCfg<DK>::SMEM <= kAloneSmem && PlainCfg<DK>::SMEM <= kAloneSmem,
+                "the chains' shared memory");
+  if (chain <= st->sms) smem = kAloneSmem;
+  if (nvfp4_status e = la_smem(st, base + (delta ? 1 : 2), kernel, kAloneSmem)) return e;
+  return launch_pdl(kernel, static_cast<unsigned>(chain),
+                    delta ? ChainCfg<DK>::THREADS : PlainCfg<DK>::THREADS, smem, s, 1u, a);
 }
 
 }  // namespace

@@ -426,13 +426,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     return;
   }
 
-  // decays and beta, requested before the keys, whose loads cover them
-  double x0 = 0.0, x1 = 0.0;
+  // decays and beta, requested before the keys, whose loads cover them (as
+  // FP32: a conversion here would wait for them)
+  float g0 = 0.0f, g1 = 0.0f;
   float bt = 0.0f;
   if (warp == 0) {
     const float* g = a.decay + tok0 * a.h_v + h;
-    if (2 * lane < len) x0 = g[static_cast<int64_t>(2 * lane) * a.h_v];
-    if (2 * lane + 1 < len) x1 = g[static_cast<int64_t>(2 * lane + 1) * a.h_v];
+    if (2 * lane < len) g0 = g[static_cast<int64_t>(2 * lane) * a.h_v];
+    if (2 * lane + 1 < len) g1 = g[static_cast<int64_t>(2 * lane + 1) * a.h_v];
   } else if (t >= 64 && t < 128 && t - 64 < len) {
     bt = a.beta != nullptr ? a.beta[(tok0 + t - 64) * a.h_v + h] : 1.0f;
   }
@@ -464,8 +465,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   if (warp == 0) {
     // G in FP64 (a decay of e^-1000 is zero, so -inf counts as that)
     constexpr double kLog2e = 1.4426950408889634;
-    x0 = (x0 < -1000.0 ? -1000.0 : x0) * kLog2e;
-    x1 = (x1 < -1000.0 ? -1000.0 : x1) * kLog2e;
+    const double x0 = (g0 < -1000.0f ? -1000.0 : static_cast<double>(g0)) * kLog2e;
+    const double x1 = (g1 < -1000.0f ? -1000.0 : static_cast<double>(g1)) * kLog2e;
     double s = x0 + x1;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {

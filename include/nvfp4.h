@@ -459,7 +459,8 @@ size_t nvfp4_linear_attention_workspace_bytes(int64_t total, int64_t n_seq, int 
  *              Value head i goes with key head i / (h_v / h_k). q, k and v may
  *              be column ranges of one fused projection.
  *   decay      device FP32 [total][h_v]: g, the log of the decay (g <= 0; -inf
- *              or anything below -1000 forgets the state).
+ *              or anything below -1000 forgets the state, which has
+ *              to be finite all the same).
  *   beta       device FP32 [total][h_v] or NULL. The delta rule is stable for
  *              beta |k|^2 <= 2; the keys are taken as they are (not normalised).
  *   total      packed tokens, >= 0.   n_seq >= 1 sequences:
@@ -484,9 +485,11 @@ size_t nvfp4_linear_attention_workspace_bytes(int64_t total, int64_t n_seq, int 
  *              initialisation needed.
  *   h_v % h_k == 0; d_k 64 or 128; d_v % 32 == 0; all row pitches multiples of
  *   8 elements; q, k, v, o, state 16-byte aligned.
- * Two kernels. The MMA operands made from FP32 values (states, the chunk's
- * factors) are split into two bf16 pieces each: states and outputs carry
- * errors of about 2^-17 of their scale before o's rounding to bf16.
+ * Two kernels. MMA operands made from FP32 values are cut into bf16 pieces:
+ * three (nothing is lost) where the new state rests on them, two (2^-18 of the
+ * value is lost) for the state itself and the chunk's factors, so states and
+ * outputs carry errors of at most about 2^-17 of their scale, before o's
+ * rounding to bf16.
  * Results do not depend on the run or on the other sequences of the call.
  * Errors: INVALID_ARG, UNSUPPORTED (d_k, d_v, sizes >= 2^31), MISALIGNED, CUDA.
  */

@@ -295,6 +295,8 @@ typedef enum {
  *               (y_dtype bf16, ldr == ldy): the residual stream is then updated
  *               in place. It may also be other columns of the matrix that Y is
  *               a part of; any other overlap with Y is refused.
+ *   X (nvfp4_linear_epilogue) must not overlap Y: a layer whose input is the
+ *   residual stream itself writes its output elsewhere.
  *   All other arguments, workspaces and launch rules as nvfp4_gemm and
  *   nvfp4_linear. The bias and the residual may be written by work that
  *   precedes the call in the stream.

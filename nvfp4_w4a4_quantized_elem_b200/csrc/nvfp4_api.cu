@@ -773,6 +773,22 @@ nvfp4_status gemm_paired(PFN_cuTensorMapEncodeTiled_v12000 enc, DeviceState* st,
                     stream, 2u, tmA, tmB, tmSFA, tmSFB, tmY, p);
 }
 
+// Whether two [rows][..] matrices share bytes: `ca` columns of `ea` bytes at
+// pitch lda, `cb` of `eb` bytes at pitch ldb. Disjoint columns of one matrix
+// (same pitch in bytes) do not.
+bool rows_overlap(const void* a, int64_t lda, int64_t ca, int64_t ea, const void* b, int64_t ldb,
+                  int64_t cb, int64_t eb, int64_t rows) {
+  if (a == nullptr || b == nullptr || rows < 1) return false;
+  const int64_t a0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a));
+  const int64_t b0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b));
+  const int64_t a1 = a0 + ((rows - 1) * lda + ca) * ea, b1 = b0 + ((rows - 1) * ldb + cb) * eb;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (rows == 1 || lda * ea != ldb * eb) return true;
+  const int64_t ld = lda * ea;
+  const int64_t d = (((b0 - a0) % ld) + ld) % ld;  // b's column offset from a, in bytes
+  return d < ca * ea || ld - d < cb * eb;
+}
+
 // Checks of an epilogue's arguments against the output they go with.
 // Y may be the residual itself (the same rows in place: every element is
 // read before it is written, by the thread that writes it), or the two may be
@@ -905,8 +921,9 @@ namespace {
 nvfp4_status linear_entry(const void* x, int64_t m, int64_t k, int64_t ldx,
                           const float* x_global, const uint8_t* w_codes, const uint8_t* w_sf,
                           const float* w_global, int64_t n, void* y, int y_dtype, int64_t ldy,
-                          void* workspace, size_t workspace_bytes, nvfp4_stream_t stream, const void* bias = nullptr,
-                          int activation = 0, const void* residual = nullptr, int64_t ldr = 0) {
+                          void* workspace, size_t workspace_bytes, nvfp4_stream_t stream,
+                          bool epilogue = false, const void* bias = nullptr, int activation = 0,
+                          const void* residual = nullptr, int64_t ldr = 0) {
   if (!x || !w_codes || !w_sf || !w_global || !y || !workspace) return NVFP4_ERR_INVALID_ARG;
   if (m < 1 || n < 1 || k < 1 || (y_dtype != 0 && y_dtype != 1) || ldy < n || ldx < k)
     return NVFP4_ERR_INVALID_ARG;
@@ -919,6 +936,9 @@ nvfp4_status linear_entry(const void* x, int64_t m, int64_t k, int64_t ldx,
       !aligned(x_global, 4) || !aligned(workspace, 256))
     return NVFP4_ERR_MISALIGNED;
   if (workspace_bytes < nvfp4_linear_workspace_bytes(m, n, k)) return NVFP4_ERR_INVALID_ARG;
+  // a residual stream updated in place is not this layer's own input: up to
+  // NVFP4_LINEAR_IN_KERNEL_MAX_TOKENS the GEMM reads X while it writes Y
+  if (epilogue && rows_overlap(x, ldx, k, 2, y, ldy, n, esize, m)) return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status e = check_epilogue(bias, activation, residual, ldr, y, y_dtype, ldy, m, n))
     return e;
   const nvfp4::epi::Args ep = epilogue_args(bias, activation, residual, ldr);
@@ -1013,7 +1033,7 @@ nvfp4_status nvfp4_linear_epilogue(const void* x, int64_t m, int64_t k, int64_t 
                                    int64_t ldy, void* workspace, size_t workspace_bytes,
                                    nvfp4_stream_t stream) {
   return linear_entry(x, m, k, ldx, x_global, w_codes, w_sf, w_global, n, y, y_dtype, ldy,
-                      workspace, workspace_bytes, stream, bias, activation, residual, ldr);
+                      workspace, workspace_bytes, stream, true, bias, activation, residual, ldr);
 }
 
 nvfp4_status nvfp4_gemm_swiglu_quant(const uint8_t* a_codes, const uint8_t* a_sf,
@@ -1179,22 +1199,6 @@ nvfp4_status nvfp4_fuse_group_scales(int n_modules, const int64_t* rows_per_modu
 }  // extern "C"
 
 namespace {
-
-// Whether two [rows][..] matrices share bytes: `ca` columns of `ea` bytes at
-// pitch lda, `cb` of `eb` bytes at pitch ldb. Disjoint columns of one matrix
-// (same pitch in bytes) do not.
-bool rows_overlap(const void* a, int64_t lda, int64_t ca, int64_t ea, const void* b, int64_t ldb,
-                  int64_t cb, int64_t eb, int64_t rows) {
-  if (a == nullptr || b == nullptr || rows < 1) return false;
-  const int64_t a0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a));
-  const int64_t b0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b));
-  const int64_t a1 = a0 + ((rows - 1) * lda + ca) * ea, b1 = b0 + ((rows - 1) * ldb + cb) * eb;
-  if (a1 <= b0 || b1 <= a0) return false;
-  if (rows == 1 || lda * ea != ldb * eb) return true;
-  const int64_t ld = lda * ea;
-  const int64_t d = (((b0 - a0) % ld) + ld) % ld;  // b's column offset from a, in bytes
-  return d < ca * ea || ld - d < cb * eb;
-}
 
 bool bytes_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return rows_overlap(a, na, na, 1, b, nb, nb, 1, 1);

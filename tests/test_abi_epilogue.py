@@ -50,6 +50,17 @@ def test_epilogue_argument_checks(L, call):
     assert call(L, n=60, ldy=60) == MISALIGNED
 
 
+def test_the_input_is_not_the_output(L):
+    """X + layer(X) into X would be read while it is written."""
+    x = FAKE * 8
+    assert lin(L, y=x, res=x) == INVALID
+    assert lin(L, m=300, y=x, res=x) == INVALID
+    assert lin(L, y=x + 64 * 2) == INVALID                # a row down
+    import torch
+    if not torch.cuda.is_available():
+        assert lin(L, y=FAKE, res=x) == CUDA              # X as the residual only
+
+
 @pytest.mark.parametrize("call", [lin, gemm])
 def test_epilogue_accepts(L, call):
     """Good arguments pass every check: without a GPU the call then fails in

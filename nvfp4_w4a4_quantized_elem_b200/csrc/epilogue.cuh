@@ -39,7 +39,7 @@ __device__ __forceinline__ float over_one_plus_ex2(float z, float t) {
 
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
-  if (ACT == kRelu) return fmaxf(z, 0.0f);
+  if (ACT == kRelu) return z < 0.0f ? 0.0f : z;  // (a NaN stays one)
   if (ACT == kSilu) return over_one_plus_ex2(z, -1.44269504f * z);
   if (ACT == kGelu) {  // erff: 2 ulp; erfcf would keep the far tail's digits at 4x the time
     const float h = 0.5f * z;

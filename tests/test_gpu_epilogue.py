@@ -162,3 +162,20 @@ def test_epilogue_in_a_graph(nv, orc, m):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, nv.linear(x, W, bias=bias, activation="gelu", residual=res))
+
+
+@pytest.mark.parametrize("m", [4, 40, 200])
+@pytest.mark.parametrize("act", ACTS)
+def test_not_a_number_stays(nv, orc, m, act):
+    """A NaN in one column's bias or one element of the residual reaches that
+    column or element, whatever the activation, and nothing else."""
+    n, k = 520, 512
+    x, W = gaussian(m, k, 1).cuda(), upload(orc.quantize(bits(gaussian(n, k, 2, 0.05))))
+    bias, res = gaussian(1, n, 4)[0].cuda(), gaussian(m, n, 3).cuda()
+    ref = nv.linear(x, W, bias=bias, activation=act, residual=res)
+    bias[77] = res[m - 1, 300] = float("nan")
+    y = nv.linear(x, W, bias=bias, activation=act, residual=res)
+    bad = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    bad[:, 77] = bad[m - 1, 300] = True
+    assert torch.equal(torch.isnan(y), bad)
+    assert torch.equal(y[~bad], ref[~bad])

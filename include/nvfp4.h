@@ -493,6 +493,9 @@ size_t nvfp4_linear_attention_workspace_bytes(int64_t total, int64_t n_seq, int 
  * outputs carry errors of at most about 2^-17 of their scale, before o's
  * rounding to bf16.
  * Results do not depend on the run or on the other sequences of the call.
+ * A NaN or an infinity in a token's inputs reaches the later tokens of its
+ * sequence, as in the formula, and also the earlier ones of its 64-token chunk
+ * (their zero factors multiply it); other sequences and heads stay clean.
  * Errors: INVALID_ARG, UNSUPPORTED (d_k, d_v, sizes >= 2^31), MISALIGNED, CUDA.
  */
 nvfp4_status nvfp4_linear_attention(const void* q, int64_t ldq, const void* k, int64_t ldk,

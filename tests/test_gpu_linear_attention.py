@@ -330,3 +330,65 @@ def test_another_stream_and_graph_replay(nv):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, (out, out1, state)))
     assert nv.read_fault() == 0
+
+
+@pytest.mark.parametrize("delta", [True, False])
+def test_no_tokens(nv, delta):
+    """A call without tokens: fresh sequences leave a zero state, resumed ones
+    theirs."""
+    hk, hv, dk, dv = 1, 2, 64, 32
+    q, k, v, decay, beta = inputs(0, hk, hv, dk, dv, 1)
+    state = torch.randn(3, hv, dk, dv, device="cuda")
+    before = state.clone()
+    cu = torch.zeros(3, dtype=torch.int32).cuda()
+    out = nv.linear_attention(q, k, v, decay, beta if delta else None, cu_seqlens=cu, state=state,
+                              resume=torch.tensor([0, 1], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert out.shape == (0, hv, dv) and nv.read_fault() == 0
+    assert not state[0].any() and torch.equal(state[1:], before[1:])
+    assert nv.linear_attention_step(q, k, v, decay, beta, state=state).shape == (0, hv, dv)
+
+
+def test_two_calls_at_once(nv):
+    """Calls on two streams, each with its own workspace and states, again and
+    again: the results are those of calls one after the other."""
+    shapes = [([900, 65, 400], 2, 4, 128, 64), ([64, 1500], 3, 6, 64, 96)]
+    work = []
+    for i, (lens, hk, hv, dk, dv) in enumerate(shapes):
+        args = inputs(sum(lens), hk, hv, dk, dv, 40 + i)
+        cu = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32).cuda()
+        pool = torch.zeros(len(lens), hv, dk, dv, device="cuda")
+        ws = torch.empty(nv.linear_attention_workspace_bytes(sum(lens), len(lens), hk, hv, dk),
+                         dtype=torch.uint8, device="cuda")
+        out = torch.empty(sum(lens), hv, dv, dtype=torch.bfloat16, device="cuda")
+        kw = dict(cu_seqlens=cu, state=pool, out=out, workspace=ws)
+        nv.linear_attention(*args, **kw)
+        torch.cuda.synchronize()
+        work.append((args, kw, out.clone(), pool.clone(), torch.cuda.Stream()))
+    for _ in range(20):
+        for args, kw, _, _, s in work:
+            nv.linear_attention(*args, stream=s, **kw)
+    torch.cuda.synchronize()
+    assert nv.read_fault() == 0
+    for _, kw, out, pool, _ in work:
+        assert torch.equal(kw["out"], out) and torch.equal(kw["state"], pool)
+
+
+@pytest.mark.parametrize("delta", [True, False])
+def test_not_a_number_stays_in_its_sequence_and_head(nv, delta):
+    lens, hk, hv, dk, dv = [100, 70, 130], 2, 4, 128, 64
+    q, k, v, decay, beta = inputs(sum(lens), hk, hv, dk, dv, 50)
+    cu = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32).cuda()
+    state = torch.zeros(3, hv, dk, dv, device="cuda")
+    beta = beta if delta else None
+    want = nv.linear_attention(q, k, v, decay, beta, cu_seqlens=cu, state=state)
+    want_state = state.clone()
+    v[165, 2, 5] = float("nan")      # token 65 of the second sequence
+    got = nv.linear_attention(q, k, v, decay, beta, cu_seqlens=cu, state=state)
+    clean = torch.ones_like(got, dtype=torch.bool)
+    clean[164:170, 2] = False        # its second chunk
+    assert torch.equal(got[clean], want[clean])
+    assert bool(torch.isnan(got[165:170, 2, 5]).all()) and bool(torch.isnan(state[1, 2, :, 5]).all())
+    keep = torch.ones_like(state, dtype=torch.bool)
+    keep[1, 2] = False
+    assert torch.equal(state[keep], want_state[keep])

@@ -223,9 +223,11 @@ class Calibrator:
 
 
 def _epilogue(bias: torch.Tensor | None, activation: str, residual: torch.Tensor | None,
-              m: int, n: int, device: torch.device):
+              m: int, n: int, out: torch.Tensor, device: torch.device):
     """Checked epilogue arguments: (bias pointer, activation code, residual
     pointer, residual row pitch)."""
+    if tuple(out.shape) != (m, n) or out.device != device:
+        raise ValueError(f"out must be [{m}, {n}] on {device}")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
     for t, name in ((bias, "bias"), (residual, "residual")):
@@ -270,7 +272,7 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out: torch.Tensor | None = None,
     if bias is not None or residual is not None or activation != "none":
         st = lib().nvfp4_gemm_epilogue(
             _ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale), _ptr(b.codes), _ptr(b.sf),
-            _ptr(b.global_scale), *_epilogue(bias, activation, residual, m, n, out.device),
+            _ptr(b.global_scale), *_epilogue(bias, activation, residual, m, n, out, a.codes.device),
             _ptr(out), y_dtype, out.stride(0), m, n, k, _ptr(workspace), ws_bytes,
             _stream(stream))
         _check(st, "nvfp4_gemm_epilogue")
@@ -393,42 +395,46 @@ def silu_mul(y: torch.Tensor, out: torch.Tensor | None = None,
 def _heads(q, k, v, decay, beta, state, out):
     """Checked arguments shared by linear_attention and its step: (h_k, h_v,
     d_k, d_v, row pitches of q, k, v and out, out)."""
-    dev = q.device
-    if dev.type != "cuda":
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("q must be a CUDA tensor")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"q is on {dev}, the current device is {torch.cuda.current_device()}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"q is on cuda:{dev}, the current device is {torch.cuda.current_device()}")
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        if t is not None and (t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 3):
-            raise ValueError(f"{name} must be {torch.bfloat16} [rows, heads, dim] on {dev}")
-    rows, hk, dk = q.shape
-    _, hv, dv = v.shape
-    if k.shape != q.shape or v.shape[0] != rows:
+        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != dev
+                              or t.dim() != 3):
+            raise ValueError(f"{name} must be {torch.bfloat16} [rows, heads, dim] on cuda:{dev}")
+    rows, hk, dk = qs = q.shape
+    vr, hv, dv = vs = v.shape
+    if k.shape != qs or vr != rows:
         raise ValueError("q and k must be [rows, h_k, d_k], v [rows, h_v, d_v]")
     for t, name, shape in ((decay, "decay", (rows, hv)), (beta, "beta", (rows, hv)),
                            (state, "state", (hv, dk, dv))):
         if t is None:
             continue
-        if t.dtype != torch.float32 or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {torch.float32} on {dev}")
+        if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {torch.float32} on cuda:{dev}")
         if (t.shape[1:] if t is state else t.shape) != shape:
             raise ValueError(f"{name} must be {'[slots] + ' if t is state else ''}{list(shape)}")
     if out is None:
-        out = torch.empty((rows, hv, dv), dtype=torch.bfloat16, device=dev)
-    elif out.shape != v.shape:
+        out = torch.empty((rows, hv, dv), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != vs:
         raise ValueError(f"out must be [{rows}, {hv}, {dv}]")
-    pitches = []
-    for t, h, d in ((q, hk, dk), (k, hk, dk), (v, hv, dv), (out, hv, dv)):
-        ld, head, one = t.stride()
-        if (d > 1 and one != 1) or (h > 1 and head != d):
-            raise ValueError("the heads of a row of q, k, v and out must be contiguous")
-        pitches.append(ld if rows > 1 else -(-h * d // 8) * 8)
-    return hk, hv, dk, dv, pitches, out
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
+    if ((dk > 1 and (sq[2] != 1 or sk[2] != 1)) or (hk > 1 and (sq[1] != dk or sk[1] != dk))
+            or (dv > 1 and (sv[2] != 1 or so[2] != 1))
+            or (hv > 1 and (sv[1] != dv or so[1] != dv))):
+        raise ValueError("the heads of a row of q, k, v and out must be contiguous")
+    if rows > 1:
+        return hk, hv, dk, dv, (sq[0], sk[0], sv[0], so[0]), out
+    ldk, ldv = -(-hk * dk // 8) * 8, -(-hv * dv // 8) * 8  # a single row's pitch is free
+    return hk, hv, dk, dv, (ldk, ldk, ldv, ldv), out
 
 
 def _int32(t: torch.Tensor | None, name: str, n: int, device) -> None:
     if t is not None:
-        if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != device:
+        if (t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous()
+                or t.device != device):
             raise ValueError(f"{name} must be a contiguous {torch.int32} vector of {n} on {device}")
 
 
@@ -460,6 +466,8 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
         need = linear_attention_workspace_bytes(total, n_seq, hk, hv, dk)
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {q.device}")
     st = lib().nvfp4_linear_attention(
         _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(decay), _ptr(beta),
         dk ** -0.5 if scale is None else scale, total, hk, hv, dk, dv, n_seq, _ptr(cu_seqlens),
@@ -560,7 +568,7 @@ def linear(x: torch.Tensor, w: NVFP4Tensor, out: torch.Tensor | None = None,
     if bias is not None or residual is not None or activation != "none":
         st = lib().nvfp4_linear_epilogue(
             _ptr(x), m, k, x.stride(0), _ptr(global_scale), _ptr(w.codes), _ptr(w.sf),
-            _ptr(w.global_scale), n, *_epilogue(bias, activation, residual, m, n, out.device),
+            _ptr(w.global_scale), n, *_epilogue(bias, activation, residual, m, n, out, x.device),
             _ptr(out), 0 if out.dtype == torch.bfloat16 else 1, out.stride(0), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _stream(stream))
         _check(st, "nvfp4_linear_epilogue")

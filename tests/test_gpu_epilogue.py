@@ -179,3 +179,22 @@ def test_not_a_number_stays(nv, orc, m, act):
     bad[:, 77] = bad[m - 1, 300] = True
     assert torch.equal(torch.isnan(y), bad)
     assert torch.equal(y[~bad], ref[~bad])
+
+
+def test_binding_refuses(nv, orc):
+    x, W = gaussian(4, 64, 1).cuda(), upload(orc.quantize(bits(gaussian(64, 64, 2))))
+    a = nv.quantize(x)
+    bias, res = torch.zeros(64, dtype=torch.bfloat16).cuda(), torch.zeros(4, 64, dtype=torch.bfloat16).cuda()
+    for call in (lambda **kw: nv.linear(x, W, **kw), lambda **kw: nv.gemm(a, W, **kw)):
+        for kw in (dict(activation="tanh"), dict(bias=bias.float()), dict(bias=bias[:32]), dict(bias=bias.cpu()),
+                   dict(bias=bias[None]), dict(residual=res[:3]), dict(residual=res.float()),
+                   dict(residual=res.cpu()), dict(residual=res.t().contiguous().t()),
+                   dict(bias=bias, out=torch.empty(3, 64, dtype=torch.bfloat16, device="cuda")),
+                   dict(bias=bias, out=torch.empty(4, 64, dtype=torch.bfloat16))):
+            with pytest.raises(ValueError):
+                call(**kw)
+        for kw in (dict(residual=res[:1].expand(4, 64)), dict(bias=bias, out=bias.expand(4, 64))):
+            with pytest.raises((ValueError, nv.NVFP4Error)):
+                call(**kw)
+    with pytest.raises(nv.NVFP4Error):
+        nv.linear(x, W, residual=x, out=x)

@@ -392,3 +392,13 @@ def test_not_a_number_stays_in_its_sequence_and_head(nv, delta):
     keep = torch.ones_like(state, dtype=torch.bool)
     keep[1, 2] = False
     assert torch.equal(state[keep], want_state[keep])
+
+
+def test_binding_refuses_a_workspace_elsewhere(nv):
+    args = inputs(70, 1, 1, 64, 32, 60)
+    need = nv.linear_attention_workspace_bytes(70, 1, 1, 1, 64)
+    for ws in (torch.empty(need, dtype=torch.uint8), torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            nv.linear_attention(*args, workspace=ws)
+    with pytest.raises(nv.NVFP4Error):
+        nv.linear_attention(*args, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))

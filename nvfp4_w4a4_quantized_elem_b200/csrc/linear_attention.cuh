@@ -123,9 +123,18 @@ __device__ __forceinline__ uint32_t mn_off(int k, int n8, int n_stride) {
 }
 
 // N FP32 values of operand row k -> PIECES bf16 pieces, `piece` bytes apart.
+// `zero`: x is known to be all zeros.
 template <int PIECES, int N>
 __device__ __forceinline__ void store_row_split(uint32_t base, int piece, int k, int n_stride,
-                                                const float (&x)[N]) {
+                                                const float (&x)[N], bool zero = false) {
+  if (zero) {
+#pragma unroll
+    for (int n8 = 0; n8 < N / 8; ++n8)
+#pragma unroll
+      for (int p = 0; p < PIECES; ++p)
+        ptx::st_shared_v4(base + p * piece + mn_off(k, n8, n_stride), 0u, 0u, 0u, 0u);
+    return;
+  }
 #pragma unroll
   for (int n8 = 0; n8 < N / 8; ++n8) {
     float r[8];
@@ -153,7 +162,15 @@ __device__ __forceinline__ uint32_t sw128(int r, int u) {
 // rows (`piece` apart).
 template <int N>
 __device__ __forceinline__ void store_image_row(uint32_t base, int piece, int r, int u0,
-                                                const float (&x)[N]) {
+                                                const float (&x)[N], bool zero) {
+  if (zero) {
+#pragma unroll
+    for (int u = 0; u < N / 8; ++u)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        ptx::st_shared_v4(base + p * piece + sw128(r, u0 + u), 0u, 0u, 0u, 0u);
+    return;
+  }
 #pragma unroll
   for (int u = 0; u < N / 8; ++u) {
     float v[8];
@@ -506,8 +523,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j0;
   const bool delta = a.beta != nullptr;
   uint8_t* const out = a.tt + (static_cast<int64_t>(slot) * a.h_v + h) * kHeadBytes;
+  // all of this warp's 32 x 32 block lies above the diagonal, of every matrix here
+  const bool above = j0 > (row | 31);
   float x[32];
-  tc_ld(lanes, x);
+  if (!above) tc_ld(lanes, x);
   if (r < C) {
     const float f = Beta[row];
     if (j0 == 0) {
@@ -519,24 +538,27 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       if (row == 0) gate[3 * C] = ptx::ex2(ge.x + ge.y);
     }
     if (delta) {
-      decay_row(x, G, row, j0, row - 1, f);
+      if (!above) {
+        decay_row(x, G, row, j0, row - 1, f);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<float4*>(L + row * kLd + j0 + j) =
-            make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<float4*>(L + row * kLd + j0 + j) =
+              make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+      }
     } else {
       // without the delta rule T = I, and A itself stands in the place of AT
 #pragma unroll
       for (int j = 0; j < 32; ++j) x[j] = j0 + j == row ? 1.0f : 0.0f;
     }
   } else {
-    decay_row(x, G, row, j0, row, 1.0f);
-    if (delta) store_image_row(sb + P::A_OFF, P::A_PIECE, row, j0 / 8, x);  // rows from a multiple of 8
+    if (!above) decay_row(x, G, row, j0, row, 1.0f);
+    if (delta) store_image_row(sb + P::A_OFF, P::A_PIECE, row, j0 / 8, x, above);  // rows from a multiple of 8
   }
   if (delta) {
     __syncthreads();
     invert_unit_lower(L, T, M, t);
     if (r < C) {
+      if (!above)
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -544,7 +566,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
       }
       // over L, which the inverse no longer needs
-      store_row_split<2>(sb + P::L_OFF + (j0 / 8) * 1024, 8192, row, 1024, x);
+      store_row_split<2>(sb + P::L_OFF + (j0 / 8) * 1024, 8192, row, 1024, x, above);
     }
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
@@ -567,7 +589,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     }
     ok = ok && warp_wait(bar, 1, abort_flag, kFaultPrepare);
     ptx::tc_fence_after();
-    if (r >= C) {
+    if (r >= C && !above) {
       float y[32];
       tc_ld(lanes, x);
       tc_ld(lanes + C, y);
@@ -577,7 +599,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     __syncthreads();  // every warp saw the product done: the image may go over T's pieces
   }
   // hi image at T_OFF, lo image at L_OFF
-  store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, r, j0 / 8, x);
+  store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, r, j0 / 8, x, above);
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();

@@ -123,18 +123,9 @@ __device__ __forceinline__ uint32_t mn_off(int k, int n8, int n_stride) {
 }
 
 // N FP32 values of operand row k -> PIECES bf16 pieces, `piece` bytes apart.
-// `zero`: x is known to be all zeros.
 template <int PIECES, int N>
 __device__ __forceinline__ void store_row_split(uint32_t base, int piece, int k, int n_stride,
-                                                const float (&x)[N], bool zero = false) {
-  if (zero) {
-#pragma unroll
-    for (int n8 = 0; n8 < N / 8; ++n8)
-#pragma unroll
-      for (int p = 0; p < PIECES; ++p)
-        ptx::st_shared_v4(base + p * piece + mn_off(k, n8, n_stride), 0u, 0u, 0u, 0u);
-    return;
-  }
+                                                const float (&x)[N]) {
 #pragma unroll
   for (int n8 = 0; n8 < N / 8; ++n8) {
     float r[8];
@@ -158,32 +149,35 @@ __device__ __forceinline__ uint32_t sw128(int r, int u) {
   return static_cast<uint32_t>(r * 128 + ((u ^ (r & 7)) << 4));
 }
 
-// N FP32 values of row r, from its 16-byte unit u0 on -> hi and lo images of the
-// rows (`piece` apart).
-template <int N>
-__device__ __forceinline__ void store_image_row(uint32_t base, int piece, int r, int u0,
-                                                const float (&x)[N], bool zero) {
-  if (zero) {
+// 32 FP32 values -> two rounded pieces each, packed in their place: of every 8
+// values 4 words of first pieces, then 4 of second ones.
+__device__ __forceinline__ void pack_row(float (&x)[32]) {
 #pragma unroll
-    for (int u = 0; u < N / 8; ++u)
+  for (int u = 0; u < 32; u += 8) {
+    uint32_t w[8];
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-        ptx::st_shared_v4(base + p * piece + sw128(r, u0 + u), 0u, 0u, 0u, 0u);
-    return;
-  }
-#pragma unroll
-  for (int u = 0; u < N / 8; ++u) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = x[8 * u + e];
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = take_rounded(v[2 * e], v[2 * e + 1]);
-      ptx::st_shared_v4(base + p * piece + sw128(r, u0 + u), w[0], w[1], w[2], w[3]);
+    for (int e = 0; e < 4; ++e) {
+      w[e] = take_rounded(x[u + 2 * e], x[u + 2 * e + 1]);
+      w[4 + e] = round_piece(x[u + 2 * e], x[u + 2 * e + 1]);
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[u + e] = __uint_as_float(w[e]);
   }
+}
+
+__device__ __forceinline__ void st_packed(uint32_t at, int piece, const float* x) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    ptx::st_shared_v4(at + p * piece, __float_as_uint(x[4 * p]), __float_as_uint(x[4 * p + 1]),
+                      __float_as_uint(x[4 * p + 2]), __float_as_uint(x[4 * p + 3]));
+}
+
+// A packed row r, from its 16-byte unit u0 on -> hi and lo images of the rows
+// (`piece` apart).
+__device__ __forceinline__ void store_image_row(uint32_t base, int piece, int r, int u0,
+                                                const float (&x)[32]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) st_packed(base + sw128(r, u0 + u), piece, &x[8 * u]);
 }
 
 template <int N>
@@ -525,8 +519,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   uint8_t* const out = a.tt + (static_cast<int64_t>(slot) * a.h_v + h) * kHeadBytes;
   // all of this warp's 32 x 32 block lies above the diagonal, of every matrix here
   const bool above = j0 > (row | 31);
-  float x[32];
-  if (!above) tc_ld(lanes, x);
+  float x[32];  // from pack_row() on, packed pieces
+  if (above) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+  } else {
+    tc_ld(lanes, x);
+  }
   if (r < C) {
     const float f = Beta[row];
     if (j0 == 0) {
@@ -549,24 +548,32 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       // without the delta rule T = I, and A itself stands in the place of AT
 #pragma unroll
       for (int j = 0; j < 32; ++j) x[j] = j0 + j == row ? 1.0f : 0.0f;
+      pack_row(x);
     }
   } else {
-    if (!above) decay_row(x, G, row, j0, row, 1.0f);
-    if (delta) store_image_row(sb + P::A_OFF, P::A_PIECE, row, j0 / 8, x, above);  // rows from a multiple of 8
+    if (!above) {
+      decay_row(x, G, row, j0, row, 1.0f);
+      pack_row(x);
+    }
+    if (delta) store_image_row(sb + P::A_OFF, P::A_PIECE, row, j0 / 8, x);  // rows from a multiple of 8
   }
   if (delta) {
     __syncthreads();
     invert_unit_lower(L, T, M, t);
     if (r < C) {
-      if (!above)
+      if (!above) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (j0 + j <= (row | 15)) v = *reinterpret_cast<const float4*>(T + row * kLd + j0 + j);
-        x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
+        for (int j = 0; j < 32; j += 4) {
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (j0 + j <= (row | 15)) v = *reinterpret_cast<const float4*>(T + row * kLd + j0 + j);
+          x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
+        }
+        pack_row(x);
       }
       // over L, which the inverse no longer needs
-      store_row_split<2>(sb + P::L_OFF + (j0 / 8) * 1024, 8192, row, 1024, x, above);
+#pragma unroll
+      for (int n8 = 0; n8 < 4; ++n8)
+        st_packed(sb + P::L_OFF + mn_off(row, j0 / 8 + n8, 1024), 8192, &x[8 * n8]);
     }
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
@@ -595,11 +602,12 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       tc_ld(lanes + C, y);
 #pragma unroll
       for (int j = 0; j < 32; ++j) x[j] += y[j];
+      pack_row(x);
     }
     __syncthreads();  // every warp saw the product done: the image may go over T's pieces
   }
   // hi image at T_OFF, lo image at L_OFF
-  store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, r, j0 / 8, x, above);
+  store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, r, j0 / 8, x);
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();

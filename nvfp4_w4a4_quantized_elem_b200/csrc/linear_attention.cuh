@@ -305,14 +305,18 @@ __device__ __forceinline__ void tile_store(float* D, int ld, const float (&acc)[
 // T = (I + L)^-1 for the strictly lower triangular L: the 16x16 diagonal blocks
 // by FP32 forward substitution, one thread per column, then twice
 // [P 0; B Q]^-1 = [P^-1 0; -Q^-1 B P^-1 Q^-1], with 16- and 32-wide blocks on split
-// tf32 tiles, one 16x8 tile a warp, zero k-steps of the triangles left out. (On
-// the FP32 units these products read shared memory 16 bytes a lane for every
-// few multiply-adds and were what bounded the whole kernel: 73% of the shared
+// tf32 tiles, 16x8 each, zero k-steps of the triangles left out. (On the FP32
+// units these products read shared memory 16 bytes a lane for every few
+// multiply-adds and were what bounded the whole kernel: 73% of the shared
 // memory's bandwidth.) T's 16x16 blocks above the diagonal are not written.
-__device__ __forceinline__ void invert_unit_lower(const float* L, float* T, float* M, int t) {
-  const int warp = t >> 5, lane = t & 31;
-  if (t < C) {
-    const int b0 = t & ~15, j = t & 15;
+//
+// The 32x32 block at (o, o), by the warp that wrote L there: no other warp is
+// waited for, and those of A work meanwhile.
+__device__ __forceinline__ void invert_block(const float* L, float* T, float* M, int o, int lane) {
+  L += o * kLd + o;
+  T += o * kLd + o;
+  {
+    const int b0 = lane & 16, j = lane & 15;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -330,36 +334,39 @@ __device__ __forceinline__ void invert_unit_lower(const float* L, float* T, floa
 #pragma unroll
     for (int i = 0; i < 16; ++i) T[(b0 + i) * kLd + b0 + j] = x[i];
   }
-  __syncthreads();
-  {
-    // blocks (1, 0) and (3, 2), two tiles of 8 columns each, by warps 0..3
-    const int o = 32 * (warp >> 1), c = 8 * (warp & 1);
-    float* const m = M + 16 * kMLd * (warp >> 1);
-    if (warp < 4) {
-      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      tile_mac(acc, L + (o + 16) * kLd + o, kLd, T + o * kLd + o + c, kLd, 2, lane);
-      tile_store(m + c, kMLd, acc, 1.0f, lane);
-    }
-    __syncthreads();
-    if (warp < 4) {
-      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      tile_mac(acc, T + (o + 16) * kLd + o + 16, kLd, m + c, kMLd, 2, lane);
-      tile_store(T + (o + 16) * kLd + o + c, kLd, acc, -1.0f, lane);
-    }
-    __syncthreads();
+  __syncwarp();
+  float acc[2][4] = {};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) tile_mac(acc[c], L + 16 * kLd, kLd, T + 8 * c, kLd, 2, lane);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) tile_store(M + 8 * c, kMLd, acc[c], 1.0f, lane);
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.0f;
+    tile_mac(acc[c], T + 16 * kLd + 16, kLd, M + 8 * c, kMLd, 2, lane);
   }
-  {
-    // the 32x32 block below: row tile i, column tile j
-    const int i = warp >> 2, j = warp & 3;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    tile_mac(acc, L + (32 + 16 * i) * kLd + 8 * j, kLd, T + 8 * j * kLd + 8 * j, kLd, 4 - j, lane);
-    tile_store(M + 16 * i * kMLd + 8 * j, kMLd, acc, 1.0f, lane);
-    __syncthreads();
-    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-    tile_mac(acc, T + (32 + 16 * i) * kLd + 32, kLd, M + 8 * j, kMLd, 2 + 2 * i, lane);
-    tile_store(T + (32 + 16 * i) * kLd + 8 * j, kLd, acc, -1.0f, lane);
-    __syncthreads();
+#pragma unroll
+  for (int c = 0; c < 2; ++c) tile_store(T + 16 * kLd + 8 * c, kLd, acc[c], -1.0f, lane);
+}
+
+// The 32x32 block below the diagonal, by all eight warps: row tile i, column
+// tile j; the second product needs both row tiles of the first.
+__device__ __forceinline__ void invert_below(const float* L, float* T, float* M, int warp,
+                                             int lane) {
+  const int i = warp >> 2, j = warp & 3;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  tile_mac(acc, L + (32 + 16 * i) * kLd + 8 * j, kLd, T + 8 * j * kLd + 8 * j, kLd, 4 - j, lane);
+  tile_store(M + 16 * i * kMLd + 8 * j, kMLd, acc, 1.0f, lane);
+  switch (j) {  // the two warps of column tile j
+    case 0: asm volatile("bar.sync 1, 64;" ::: "memory"); break;
+    case 1: asm volatile("bar.sync 2, 64;" ::: "memory"); break;
+    case 2: asm volatile("bar.sync 3, 64;" ::: "memory"); break;
+    default: asm volatile("bar.sync 4, 64;" ::: "memory"); break;
   }
+  acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+  tile_mac(acc, T + (32 + 16 * i) * kLd + 32, kLd, M + 8 * j, kMLd, 2 + 2 * i, lane);
+  tile_store(T + (32 + 16 * i) * kLd + 8 * j, kLd, acc, -1.0f, lane);
 }
 
 // x[j] (column j0 + j) *= f e^{G_t - G_j} up to column `last`, zero beyond (a
@@ -392,12 +399,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bar + 1);
   volatile uint32_t* const abort_flag = tmem_holder + 1;
+  int2* const found = reinterpret_cast<int2*>(bar + 2);  // the chunk's first token, its tokens
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int h = blockIdx.x % a.h_v, group = a.h_v / a.h_k, hk = h / group;
   const int slot = blockIdx.x / a.h_v;
   if (t == 0) {
     ptx::mbar_init(bar, 1);
+    *found = make_int2(0, 0);
     // the swizzled images need the alignment that the declaration asks for
     *abort_flag = (ptx::smem_u32(smem) & 1023u) != 0u ? 1u : 0u;
     if (*abort_flag) atomicOr(&g_fault_word, kFaultPrepare);
@@ -412,23 +421,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   __syncthreads();
   ptx::grid_dep_launch();
   ptx::grid_dep_wait();
-  // the last sequence whose first slot is at or below this one: the slots of
-  // later sequences are higher, so it is the count of those, less one
-  int seq = -1, start = 0, end = 0;
-  for (int i = 0; i < a.n_seq; i += kPrepThreads) {
-    bool below = false;
-    if (i + t < a.n_seq) {
-      seq_range(a, i + t, start, end);
-      below = first_slot(start, i + t) <= slot;
-    }
-    const int n = __syncthreads_count(below);
-    seq += n;
-    if (n < kPrepThreads) break;
+  // the sequence that has this slot, if one does
+  for (int i = t; i < a.n_seq; i += kPrepThreads) {
+    int start, end;
+    seq_range(a, i, start, end);
+    const int64_t c = slot - first_slot(start, i), left = end - start - c * C;
+    if (c >= 0 && left > 0)
+      *found = make_int2(start + static_cast<int>(c) * C, static_cast<int>(min(left, int64_t{C})));
   }
-  if (seq >= 0) seq_range(a, seq, start, end);
-  const int64_t tok0 = start + static_cast<int64_t>(slot - first_slot(start, seq)) * C;
-  const int len = seq < 0 || tok0 < start || tok0 >= end
-                      ? 0 : static_cast<int>(min(static_cast<int64_t>(C), end - tok0));
+  __syncthreads();
+  const int64_t tok0 = found->x;
+  const int len = found->y;
   if (len == 0) {  // a slot between two sequences' chunks
     ptx::tc_fence_before();
     __syncthreads();
@@ -543,6 +546,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         for (int j = 0; j < 32; j += 4)
           *reinterpret_cast<float4*>(L + row * kLd + j0 + j) =
               make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        if (j0 == (row & 32)) {  // warps 0 and 5: the blocks on the diagonal
+          __syncwarp();
+          invert_block(L, T, M + 16 * kMLd * (j0 >> 5), j0, lane);
+        }
       }
     } else {
       // without the delta rule T = I, and A itself stands in the place of AT
@@ -559,7 +566,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   }
   if (delta) {
     __syncthreads();
-    invert_unit_lower(L, T, M, t);
+    invert_below(L, T, M, warp, lane);
+    __syncthreads();
     if (r < C) {
       if (!above) {
 #pragma unroll
@@ -615,7 +623,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     ptx::bulk_store(out, smem + P::T_OFF, kTTBytes);
     ptx::bulk_store(out + kTTBytes, smem + P::L_OFF, kTTBytes);
     ptx::bulk_commit_group();
-    ptx::bulk_wait_group_all();
+    // (the grid's end waits for the writes; the CTA only for its shared memory)
+    ptx::bulk_wait_group_read<0>();
   }
   ptx::tc_fence_after();
   if (warp == 1) {

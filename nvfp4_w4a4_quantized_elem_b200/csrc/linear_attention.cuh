@@ -23,7 +23,12 @@
 // does not depend on S: the swizzled bf16 image of [K; Q] (rows past a
 // sequence's end zero), [T; AT] and the decay factors. chain_kernel walks a
 // sequence's chunks in order, one CTA per (sequence, head, d_v block), with S
-// in FP32 registers.
+// in FP32 registers; plain_kernel takes its place without the delta rule.
+// Measured: 8192 tokens, 16 key and 32 value heads of 128: prepare 96 us, chain
+// 330 us (128 steps of 2.5 us); 7777 tokens in 23 prompts, 48 value heads: 147
+// and 390 us under the profiler, 500 together; 4096 tokens in 3 prompts, 24 heads
+// of 64 x 128 without the delta rule: 22 and 70 us. All of them are bound by
+// latency, the chains by that of their dependent products.
 //
 // Precision: q, k, v are bf16 and enter the products exactly. FP32 operands are
 // cut into bf16 pieces, products accumulated in FP32. X and U~, on which the
@@ -244,8 +249,9 @@ constexpr int kMBytes = 32 * kMLd * 4;
 // [T; AT] image over T and, the product A T done, over T's pieces. A's pieces
 // are the rows 64..127 of 128-row operands whose rows 0..63 lie in whatever
 // stands before them: those rows of the product are not read. Four CTAs of 256
-// threads per SM: the kernel is a chain of short dependent phases, and what
-// fills their gaps is other CTAs.
+// threads per SM: the kernel is a chain of short dependent phases (20 K cycles
+// a CTA among four: 5 K for K and Q to arrive, 6 K for L and its inverse), and
+// what fills their gaps is other CTAs.
 template <int DK>
 struct PrepCfg {
   static constexpr int KQ = kq_bytes(DK);

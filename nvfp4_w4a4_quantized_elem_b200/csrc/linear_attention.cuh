@@ -557,11 +557,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
           invert_block(L, T, M + 16 * kMLd * (j0 >> 5), j0, lane);
         }
       }
-    } else {
-      // without the delta rule T = I, and A itself stands in the place of AT
-#pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = j0 + j == row ? 1.0f : 0.0f;
-      pack_row(x);
     }
   } else {
     if (!above) {
@@ -620,14 +615,16 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     }
     __syncthreads();  // every warp saw the product done: the image may go over T's pieces
   }
-  // hi image at T_OFF, lo image at L_OFF
-  store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, r, j0 / 8, x);
+  // hi image at T_OFF, lo image at L_OFF; without the delta rule A itself stands
+  // in the place of AT, and T = I is left out
+  if (delta || r >= C) store_image_row(sb + P::T_OFF, P::L_OFF - P::T_OFF, r, j0 / 8, x);
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();
   if (t == 0) {
-    ptx::bulk_store(out, smem + P::T_OFF, kTTBytes);
-    ptx::bulk_store(out + kTTBytes, smem + P::L_OFF, kTTBytes);
+    const int skip = delta ? 0 : kTTBytes / 2;
+    ptx::bulk_store(out + skip, smem + P::T_OFF + skip, kTTBytes - skip);
+    ptx::bulk_store(out + kTTBytes + skip, smem + P::L_OFF + skip, kTTBytes - skip);
     ptx::bulk_commit_group();
     // (the grid's end waits for the writes; the CTA only for its shared memory)
     ptx::bulk_wait_group_read<0>();
@@ -975,7 +972,7 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
 // own chain is S' = e^{G_64} S + K^T U~ in registers. So A V and K^T U~ of a chunk
 // run while its state is cut into pieces and the chunk before is written out,
 // and a step takes one product's latency instead of three. V enters in one
-// piece (exact). Of the [I; A] image only the rows of A are loaded: the product's
+// piece (exact). Of the image only the rows of A are there: the product's
 // rows 0..63, which would be V itself, come from whatever stands before them in
 // shared memory and are not read. The rest is chain_kernel's.
 template <int DK>

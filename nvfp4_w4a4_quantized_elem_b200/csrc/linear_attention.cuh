@@ -975,40 +975,45 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
 // piece (exact). Of the image only the rows of A are there: the product's
 // rows 0..63, which would be V itself, come from whatever stands before them in
 // shared memory and are not read. The rest is chain_kernel's.
-template <int DK>
+// With 128 of d_k two CTAs fit an SM only if A has one buffer (A_BUFS), asked for
+// when the product before is complete: 8192 tokens of 64 heads take 360 us so,
+// 523 with two buffers and one CTA per SM; where the CTAs are no more than the
+// SMs, two buffers take 277 us for 32 heads, one 289.
+template <int DK, int A_BUFS>
 struct PlainCfg {
   static constexpr int WARPS = 4 * (DVB / kCols);
   static constexpr int THREADS = 32 * WARPS + 32;
   static constexpr int S_PIECE = DK * DVB * 2;
   static constexpr int X_PIECE = C * DVB * 2;
   static constexpr int A_BYTES = kTTBytes / 2;       // one piece of A
-  static constexpr int A_OFF = 2 * kq_bytes(DK);     // [2][2] pieces
-  static constexpr int S_OFF = A_OFF + 4 * A_BYTES;
+  static constexpr int A_OFF = 2 * kq_bytes(DK);     // [A_BUFS][2] pieces
+  static constexpr int S_OFF = A_OFF + A_BUFS * 2 * A_BYTES;
   static constexpr int V_OFF = S_OFF + kSPieces * S_PIECE;
   static constexpr int U_OFF = V_OFF + X_PIECE;
   static constexpr int BAR_OFF = U_OFF + kPieces * X_PIECE;
   static constexpr int SMEM = BAR_OFF + 128;   // the base is 1024-byte aligned
-  static constexpr int PER_SM = DK == 64 ? 2 : 1;
   // tensor memory: Q S (with K S), A V (with I V), K^T U~
   static constexpr uint32_t D1 = 0, D2 = kSPieces * DVB, D3 = D2 + DVB;
   static constexpr uint32_t TMEM = 256;
-  static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024 && SMEM <= 227 * 1024 &&
-                    D3 + kPieces * DVB <= TMEM, "CTAs per SM");
+  static constexpr int PER_SM = DK == 64 || A_BUFS == 1 ? 2 : 1;
+  static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024 && D3 + kPieces * DVB <= TMEM, "CTAs per SM");
 };
 
-template <int DK>
-__global__ void __launch_bounds__(PlainCfg<DK>::THREADS, PlainCfg<DK>::PER_SM)
+template <int DK, int A_BUFS>
+__global__ void __launch_bounds__(PlainCfg<DK, A_BUFS>::THREADS, PlainCfg<DK, A_BUFS>::PER_SM)
     plain_kernel(const Args a) {
-  using P = PlainCfg<DK>;
+  using P = PlainCfg<DK, A_BUFS>;
   extern __shared__ __align__(1024) uint8_t smem_la[];
   uint8_t* const smem = smem_la;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);  // [2] K; Q and A loaded
-  uint64_t* const v_ready = full + 2;   // V and U~ written, A V and K^T U~ before them taken
-  uint64_t* const s_ready = full + 3;   // S written, Q S before it taken
-  uint64_t* const d1 = full + 4;        // Q S complete
-  uint64_t* const d23 = full + 5;       // A V and K^T U~ complete
-  uint64_t* const drain = full + 6;
-  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(full + 7);
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);  // [2] K; Q loaded
+  uint64_t* const full_a = full + 2;    // [A_BUFS] A loaded
+  uint64_t* const v_ready = full + 4;   // V and U~ written, A V and K^T U~ before them taken
+  uint64_t* const s_ready = full + 5;   // S written, Q S before it taken
+  uint64_t* const d1 = full + 6;        // Q S, A V, K^T U~ complete
+  uint64_t* const d2 = full + 7;
+  uint64_t* const d3 = full + 8;
+  uint64_t* const drain = full + 9;
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(full + 10);
   volatile uint32_t* const abort_flag = tmem_holder + 1;
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -1021,10 +1026,12 @@ __global__ void __launch_bounds__(PlainCfg<DK>::THREADS, PlainCfg<DK>::PER_SM)
   if (t == 0) {
     ptx::mbar_init(&full[0], 1);
     ptx::mbar_init(&full[1], 1);
+    for (int i = 0; i < A_BUFS; ++i) ptx::mbar_init(&full_a[i], 1);
     ptx::mbar_init(v_ready, P::WARPS);
     ptx::mbar_init(s_ready, P::WARPS);
     ptx::mbar_init(d1, 1);
-    ptx::mbar_init(d23, 1);
+    ptx::mbar_init(d2, 1);
+    ptx::mbar_init(d3, 1);
     ptx::mbar_init(drain, 1);
     // the swizzled images need the alignment that the declaration asks for
     *abort_flag = (ptx::smem_u32(smem) & 1023u) != 0u ? 1u : 0u;
@@ -1050,15 +1057,18 @@ __global__ void __launch_bounds__(PlainCfg<DK>::THREADS, PlainCfg<DK>::PER_SM)
   // every barrier's phase c is chunk c's
   if (warp == kMmaWarp) {
     if (lane == 0) {
-      auto load = [&](int c) {
-        uint64_t* bar = &full[c & 1];
-        uint8_t* const pieces = smem + P::A_OFF + (c & 1) * 2 * P::A_BYTES;
-        const uint8_t* const image =
-            a.tt + ((static_cast<int64_t>(slot0) + c) * a.h_v + h) * kHeadBytes + P::A_BYTES;
-        ptx::mbar_arrive_expect_tx(bar, kq_bytes(DK) + 2 * P::A_BYTES);
+      auto load_kq = [&](int c) {
+        ptx::mbar_arrive_expect_tx(&full[c & 1], kq_bytes(DK));
         ptx::bulk_load(smem + (c & 1) * kq_bytes(DK),
                        a.kq + ((static_cast<int64_t>(slot0) + c) * a.h_k + hk) * kq_bytes(DK),
-                       kq_bytes(DK), bar);
+                       kq_bytes(DK), &full[c & 1]);
+      };
+      auto load_a = [&](int c) {
+        const uint8_t* const image =
+            a.tt + ((static_cast<int64_t>(slot0) + c) * a.h_v + h) * kHeadBytes + P::A_BYTES;
+        uint8_t* const pieces = smem + P::A_OFF + c % A_BUFS * 2 * P::A_BYTES;
+        uint64_t* const bar = &full_a[c % A_BUFS];
+        ptx::mbar_arrive_expect_tx(bar, 2 * P::A_BYTES);
         ptx::bulk_load(pieces, image, P::A_BYTES, bar);
         ptx::bulk_load(pieces + P::A_BYTES, image + kTTBytes, P::A_BYTES, bar);
       };
@@ -1066,16 +1076,18 @@ __global__ void __launch_bounds__(PlainCfg<DK>::THREADS, PlainCfg<DK>::PER_SM)
       constexpr uint32_t kI2 = ptx::idesc_bf16(128, DVB, false, true);
       constexpr uint32_t kI3 = ptx::idesc_bf16(128, kPieces * DVB, true, true);
       constexpr uint32_t kSN = DK * 16, kXN = C * 16;  // bytes between groups of 8 columns
-      int asked = 0, arrived = 0;  // chunks
+      int kq_asked = 0, kq_seen = 0, a_asked = 0, a_seen = 0;  // chunks
       bool ok = *abort_flag == 0u;
-      if (n > 0 && ok) load(asked++);
+      if (n > 0 && ok) {
+        load_kq(kq_asked++);
+        load_a(a_asked++);
+      }
       for (int c = 0; c < n && ok; ++c) {
         const uint32_t par = c & 1;
         const uint32_t kq = sb + par * kq_bytes(DK);
-        const uint32_t pieces = sb + P::A_OFF + par * 2 * P::A_BYTES;
         ok = wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma);
         if (!ok) break;
-        ++arrived;
+        ++kq_seen;
         ok = wait_bounded(v_ready, par, abort_flag, kFaultChainMma);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -1084,6 +1096,11 @@ __global__ void __launch_bounds__(PlainCfg<DK>::THREADS, PlainCfg<DK>::PER_SM)
           ptx::tc_mma_bf16(tmem + P::D3,
                            ptx::smem_desc(kq + s * 2048, DK == 128 ? kHalfBytes : 0, 1024, 2),
                            ptx::smem_desc(sb + P::U_OFF + s * 256, 128, kXN, 0), kI3, s != 0);
+        ptx::tc_commit(d3);
+        const uint32_t pieces = sb + P::A_OFF + c % A_BUFS * 2 * P::A_BYTES;
+        ok = wait_bounded(&full_a[c % A_BUFS], (c / A_BUFS) & 1, abort_flag, kFaultChainMma);
+        if (!ok) break;
+        ++a_seen;
 #pragma unroll
         for (int p = 0; p < 2; ++p)        // [*; A] V, A in two pieces
 #pragma unroll
@@ -1091,23 +1108,30 @@ __global__ void __launch_bounds__(PlainCfg<DK>::THREADS, PlainCfg<DK>::PER_SM)
             ptx::tc_mma_bf16(tmem + P::D2,
                              ptx::smem_desc(pieces + (p - 1) * P::A_BYTES + s * 32, 16, 1024, 2),
                              ptx::smem_desc(sb + P::V_OFF + s * 256, 128, kXN, 0), kI2, (p | s) != 0);
-        ptx::tc_commit(d23);
+        ptx::tc_commit(d2);
         ok = wait_bounded(s_ready, par, abort_flag, kFaultChainMma);
         if (!ok) break;
         // S in place: Q S of the chunk before is taken, and with it the last
         // reader of the other buffers complete
-        if (c + 1 < n) load(asked++);
+        if (c + 1 < n) load_kq(kq_asked++);
+        if (A_BUFS > 1 && c + 1 < n) load_a(a_asked++);
         ptx::tc_fence_after();
 #pragma unroll
         for (int s = 0; s < DK / 16; ++s)   // [K; Q] S
           ptx::tc_mma_bf16(tmem + P::D1, ptx::smem_desc(kq + (s / 4) * kHalfBytes + (s % 4) * 32, 16, 1024, 2),
                            ptx::smem_desc(sb + P::S_OFF + s * 256, 128, kSN, 0), kI1, s != 0);
         ptx::tc_commit(d1);
+        if (A_BUFS == 1 && c + 1 < n) {
+          ok = wait_bounded(d2, par, abort_flag, kFaultChainMma);
+          if (!ok) break;
+          load_a(a_asked++);
+        }
       }
       if (!ok) {  // let what is in flight end before the CTA does
         ptx::tc_commit(drain);
         drain_wait(drain, 0);
-        for (int c = arrived; c < asked; ++c) drain_wait(&full[c & 1], (c >> 1) & 1);
+        for (int c = kq_seen; c < kq_asked; ++c) drain_wait(&full[c & 1], (c >> 1) & 1);
+        for (int c = a_seen; c < a_asked; ++c) drain_wait(&full_a[c % A_BUFS], (c / A_BUFS) & 1);
       } else if (n > 0) {
         drain_wait(d1, (n - 1) & 1);  // the last product, should the others give up on it
       }
@@ -1160,9 +1184,11 @@ __global__ void __launch_bounds__(PlainCfg<DK>::THREADS, PlainCfg<DK>::PER_SM)
       const uint32_t par = c & 1, before = par ^ 1;
       float D[kCols], AV[kCols];
       if (c > 0) {
-        if (!(ok = warp_wait(d23, before, abort_flag, kFaultChain))) break;
+        if (!(ok = warp_wait(d3, before, abort_flag, kFaultChain))) break;
         ptx::tc_fence_after();
         ld_sum<kPieces>(lanes + P::D3, D);
+        if (!(ok = warp_wait(d2, before, abort_flag, kFaultChain))) break;
+        ptx::tc_fence_after();
         if (!is_v) {
           ptx::tc_ld_32x32b_x16(lanes + P::D2, AV);
           ptx::tc_wait_ld();

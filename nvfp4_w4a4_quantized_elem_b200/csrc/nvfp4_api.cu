@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -1252,7 +1253,7 @@ nvfp4_status la_smem(DeviceState* st, unsigned bit, K kernel, int bytes) {
 template <int DK>
 nvfp4_status launch_linear_attention(DeviceState* st, const nvfp4::la::Args& a, cudaStream_t s) {
   using namespace nvfp4::la;
-  const unsigned base = DK == 128 ? 0u : 3u;
+  const unsigned base = DK == 128 ? 0u : 4u;
   const int64_t prep = chunk_slots(a.total, a.n_seq) * a.h_v;
   const int64_t chain = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / DVB);
   if (prep >= (int64_t{1} << 31) || chain >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
@@ -1260,19 +1261,22 @@ nvfp4_status launch_linear_attention(DeviceState* st, const nvfp4::la::Args& a, 
   if (nvfp4_status e = launch_pdl(prepare_kernel<DK>, static_cast<unsigned>(prep), kPrepThreads,
                                   PrepCfg<DK>::SMEM, s, 1u, a))
     return e;
-  const bool delta = a.beta != nullptr;
-  const auto kernel = delta ? chain_kernel<DK> : plain_kernel<DK>;
-  int smem = delta ? ChainCfg<DK>::SMEM : PlainCfg<DK>::SMEM;
-  // At most one CTA per SM's worth: asking for more than half of an SM's shared
-  // memory keeps them apart (they start while the first kernel's CTAs leave, and
-  // two on one SM then took 8192 tokens of 32 heads from 447 to 561 us).
-  constexpr int kAloneSmem = 130 * 1024;
-  static_assert(ChainCfg<DK>::SMEM <= kAloneSmem && PlainCfg<DK>::SMEM <= kAloneSmem,
-                "the chains' shared memory");
-  if (chain <= st->sms) smem = kAloneSmem;
-  if (nvfp4_status e = la_smem(st, base + (delta ? 1 : 2), kernel, kAloneSmem)) return e;
-  return launch_pdl(kernel, static_cast<unsigned>(chain),
-                    delta ? ChainCfg<DK>::THREADS : PlainCfg<DK>::THREADS, smem, s, 1u, a);
+  const auto run = [&](auto kernel, unsigned bit, int threads, int bytes) -> nvfp4_status {
+    // At most one CTA per SM's worth: asking for more than half of an SM's shared
+    // memory keeps them apart (they start while the first kernel's CTAs leave, and
+    // two on one SM then took 8192 tokens of 32 heads from 447 to 561 us).
+    constexpr int kAloneSmem = 130 * 1024;
+    if (chain <= st->sms && bytes < kAloneSmem) bytes = kAloneSmem;
+    if (nvfp4_status e = la_smem(st, base + bit, kernel, std::max(bytes, kAloneSmem))) return e;
+    return launch_pdl(kernel, static_cast<unsigned>(chain), threads, bytes, s, 1u, a);
+  };
+  if (a.beta != nullptr)
+    return run(chain_kernel<DK>, 1, ChainCfg<DK>::THREADS, ChainCfg<DK>::SMEM);
+  // one buffer of A where two would leave an SM one CTA (plain_kernel's comment)
+  if (DK == 128 && chain > st->sms)
+    return run(plain_kernel<DK, DK == 128 ? 1 : 2>, 2, PlainCfg<DK, 1>::THREADS,
+               PlainCfg<DK, 1>::SMEM);
+  return run(plain_kernel<DK, 2>, 3, PlainCfg<DK, 2>::THREADS, PlainCfg<DK, 2>::SMEM);
 }
 
 }  // namespace

@@ -639,8 +639,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 // -------------------------------------------------------------------- chain --
 
 constexpr int kSPieces = 2, kPieces = 3;   // of S; of X and U~
-constexpr int DVB = 32;                    // columns of d_v per CTA
-constexpr int kCols = 16;                  // of them per compute thread
+constexpr int kCols = 16;                  // columns of d_v per compute thread
 
 // The pieces of an operand lie side by side on the N side, [hi | mid | lo], and
 // the reader adds the column blocks of the result: an MMA with 128 rows and K
@@ -656,7 +655,11 @@ constexpr int kCols = 16;                  // of them per compute thread
 // [T; AT] has one buffer (reloaded behind its product, two products ahead of
 // its next use), only [K; Q] two. D1 and D3 share tensor-memory columns. 64
 // columns per CTA and one CTA per SM took 6.8 K cycles per step.
-template <int DK>
+// DVB columns of d_v per CTA: 32, or 16 where those CTAs are no more than the
+// SMs. The MMAs read their 128 rows from shared memory whatever their columns,
+// so 16 do not halve a step, but shorten it: 8192 tokens of 8 and 16 heads of 128
+// take 306 and 330 us, 356 and 381 with 32 columns; of 32 heads 461 against 426.
+template <int DK, int DVB>
 struct ChainCfg {
   static constexpr int WARPS = 4 * (DVB / kCols);
   static constexpr int THREADS = 32 * WARPS + 32;
@@ -669,7 +672,7 @@ struct ChainCfg {
   static constexpr int BAR_OFF = R_OFF + R_BYTES;
   static constexpr int SMEM = BAR_OFF + 128;   // the base is 1024-byte aligned
   static constexpr uint32_t D2_COL = kPieces * DVB;
-  static constexpr uint32_t TMEM = 256;
+  static constexpr uint32_t TMEM = DVB == 32 ? 256 : 128;
   static_assert(2 * (SMEM + 1024) <= 228 * 1024 && 2 * D2_COL <= TMEM, "two CTAs per SM");
 };
 
@@ -721,7 +724,7 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* o, float scale, float e
 }
 
 // This thread's 16 columns of the BLOCKS column blocks of a result, added.
-template <int BLOCKS>
+template <int BLOCKS, int DVB>
 __device__ __forceinline__ void ld_sum(uint32_t taddr, float (&x)[kCols]) {
   float y[BLOCKS - 1][kCols];
   ptx::tc_ld_32x32b_x16(taddr, x);
@@ -734,10 +737,10 @@ __device__ __forceinline__ void ld_sum(uint32_t taddr, float (&x)[kCols]) {
     for (int i = 0; i < BLOCKS - 1; ++i) x[j] += y[i][j];
 }
 
-template <int DK>
-__global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
+template <int DK, int DVB>
+__global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
     chain_kernel(const Args a) {
-  using P = ChainCfg<DK>;
+  using P = ChainCfg<DK, DVB>;
   extern __shared__ __align__(1024) uint8_t smem_la[];
   uint8_t* const smem = smem_la;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);  // [2] K; Q loaded
@@ -918,7 +921,7 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
       float D[kCols], Q[kCols];
       if (!(ok = warp_wait(d1, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      ld_sum<kSPieces>(lanes, Q);
+      ld_sum<kSPieces, DVB>(lanes, Q);
       if (is_k) {
 #pragma unroll
         for (int u = 0; u < kCols / 8; ++u) {
@@ -939,7 +942,7 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
       if (c + 1 < n) fetch(c + 1);
       if (!(ok = warp_wait(d2, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      ld_sum<kPieces>(lanes + P::D2_COL, D);
+      ld_sum<kPieces, DVB>(lanes + P::D2_COL, D);
       if (is_k) {
 #pragma unroll
         for (int j = 0; j < kCols; ++j) D[j] *= erest_c;
@@ -950,7 +953,7 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
       }
       if (!(ok = warp_wait(d3, par, abort_flag, kFaultChain))) break;
       ptx::tc_fence_after();
-      ld_sum<kPieces>(lanes, D);
+      ld_sum<kPieces, DVB>(lanes, D);
 #pragma unroll
       for (int j = 0; j < kCols; ++j) S[j] = eall_c * S[j] + D[j];
     }
@@ -978,8 +981,9 @@ __global__ void __launch_bounds__(ChainCfg<DK>::THREADS, 2)
 // With 128 of d_k two CTAs fit an SM only if A has one buffer (A_BUFS), asked for
 // when the product before is complete: 8192 tokens of 64 heads take 360 us so,
 // 523 with two buffers and one CTA per SM; where the CTAs are no more than the
-// SMs, two buffers take 277 us for 32 heads, one 289.
-template <int DK, int A_BUFS>
+// SMs, two buffers take 277 us for 32 heads, one 289. DVB as chain_kernel's: 8192
+// tokens of 8 heads take 193 us with 16 columns, 207 with 32.
+template <int DK, int DVB, int A_BUFS>
 struct PlainCfg {
   static constexpr int WARPS = 4 * (DVB / kCols);
   static constexpr int THREADS = 32 * WARPS + 32;
@@ -994,15 +998,16 @@ struct PlainCfg {
   static constexpr int SMEM = BAR_OFF + 128;   // the base is 1024-byte aligned
   // tensor memory: Q S (with K S), A V (with I V), K^T U~
   static constexpr uint32_t D1 = 0, D2 = kSPieces * DVB, D3 = D2 + DVB;
-  static constexpr uint32_t TMEM = 256;
+  static constexpr uint32_t TMEM = DVB == 32 ? 256 : 128;
   static constexpr int PER_SM = DK == 64 || A_BUFS == 1 ? 2 : 1;
   static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024 && D3 + kPieces * DVB <= TMEM, "CTAs per SM");
 };
 
-template <int DK, int A_BUFS>
-__global__ void __launch_bounds__(PlainCfg<DK, A_BUFS>::THREADS, PlainCfg<DK, A_BUFS>::PER_SM)
+template <int DK, int DVB, int A_BUFS>
+__global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
+                                  PlainCfg<DK, DVB, A_BUFS>::PER_SM)
     plain_kernel(const Args a) {
-  using P = PlainCfg<DK, A_BUFS>;
+  using P = PlainCfg<DK, DVB, A_BUFS>;
   extern __shared__ __align__(1024) uint8_t smem_la[];
   uint8_t* const smem = smem_la;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::BAR_OFF);  // [2] K; Q loaded
@@ -1186,7 +1191,7 @@ __global__ void __launch_bounds__(PlainCfg<DK, A_BUFS>::THREADS, PlainCfg<DK, A_
       if (c > 0) {
         if (!(ok = warp_wait(d3, before, abort_flag, kFaultChain))) break;
         ptx::tc_fence_after();
-        ld_sum<kPieces>(lanes + P::D3, D);
+        ld_sum<kPieces, DVB>(lanes + P::D3, D);
         if (!(ok = warp_wait(d2, before, abort_flag, kFaultChain))) break;
         ptx::tc_fence_after();
         if (!is_v) {
@@ -1221,7 +1226,7 @@ __global__ void __launch_bounds__(PlainCfg<DK, A_BUFS>::THREADS, PlainCfg<DK, A_
         if (!(ok = warp_wait(d1, before, abort_flag, kFaultChain))) break;
         ptx::tc_fence_after();
       }
-      if (c > 0 && !is_v) ld_sum<kSPieces>(lanes + P::D1, D);  // Q S
+      if (c > 0 && !is_v) ld_sum<kSPieces, DVB>(lanes + P::D1, D);  // Q S
       if (c < n) {
         if (DK == 128 || k_row < DK) store_row_split<kSPieces>(r_s, P::S_PIECE, k_row, DK * 16, S);
         publish(s_ready);

@@ -1253,30 +1253,43 @@ nvfp4_status la_smem(DeviceState* st, unsigned bit, K kernel, int bytes) {
 template <int DK>
 nvfp4_status launch_linear_attention(DeviceState* st, const nvfp4::la::Args& a, cudaStream_t s) {
   using namespace nvfp4::la;
-  const unsigned base = DK == 128 ? 0u : 4u;
+  const unsigned base = DK == 128 ? 0u : 8u;
   const int64_t prep = chunk_slots(a.total, a.n_seq) * a.h_v;
-  const int64_t chain = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / DVB);
-  if (prep >= (int64_t{1} << 31) || chain >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
+  const int64_t chains = static_cast<int64_t>(a.n_seq) * a.h_v * (a.d_v / 32);
+  if (prep >= (int64_t{1} << 31) || chains >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
   if (nvfp4_status e = la_smem(st, base, prepare_kernel<DK>, PrepCfg<DK>::SMEM)) return e;
   if (nvfp4_status e = launch_pdl(prepare_kernel<DK>, static_cast<unsigned>(prep), kPrepThreads,
                                   PrepCfg<DK>::SMEM, s, 1u, a))
     return e;
-  const auto run = [&](auto kernel, unsigned bit, int threads, int bytes) -> nvfp4_status {
+  const auto run = [&](auto kernel, unsigned bit, int64_t grid, int threads,
+                       int bytes) -> nvfp4_status {
     // At most one CTA per SM's worth: asking for more than half of an SM's shared
     // memory keeps them apart (they start while the first kernel's CTAs leave, and
     // two on one SM then took 8192 tokens of 32 heads from 447 to 561 us).
     constexpr int kAloneSmem = 130 * 1024;
-    if (chain <= st->sms && bytes < kAloneSmem) bytes = kAloneSmem;
-    if (nvfp4_status e = la_smem(st, base + bit, kernel, std::max(bytes, kAloneSmem))) return e;
-    return launch_pdl(kernel, static_cast<unsigned>(chain), threads, bytes, s, 1u, a);
+    const int most = std::max(bytes, kAloneSmem);
+    if (nvfp4_status e = la_smem(st, base + bit, kernel, most)) return e;
+    return launch_pdl(kernel, static_cast<unsigned>(grid), threads, grid <= st->sms ? most : bytes,
+                      s, 1u, a);
   };
+  // 16 columns of d_v per CTA where those CTAs are no more than the SMs, and with
+  // 128 of d_k one buffer of A where two would leave an SM one CTA: both sides
+  // measured at the kernels
+  const bool narrow = 2 * chains <= st->sms;
   if (a.beta != nullptr)
-    return run(chain_kernel<DK>, 1, ChainCfg<DK>::THREADS, ChainCfg<DK>::SMEM);
-  // one buffer of A where two would leave an SM one CTA (plain_kernel's comment)
-  if (DK == 128 && chain > st->sms)
-    return run(plain_kernel<DK, DK == 128 ? 1 : 2>, 2, PlainCfg<DK, 1>::THREADS,
-               PlainCfg<DK, 1>::SMEM);
-  return run(plain_kernel<DK, 2>, 3, PlainCfg<DK, 2>::THREADS, PlainCfg<DK, 2>::SMEM);
+    return narrow ? run(chain_kernel<DK, 16>, 1, 2 * chains, ChainCfg<DK, 16>::THREADS,
+                        ChainCfg<DK, 16>::SMEM)
+                  : run(chain_kernel<DK, 32>, 2, chains, ChainCfg<DK, 32>::THREADS,
+                        ChainCfg<DK, 32>::SMEM);
+  if (narrow)
+    return run(plain_kernel<DK, 16, 2>, 3, 2 * chains, PlainCfg<DK, 16, 2>::THREADS,
+               PlainCfg<DK, 16, 2>::SMEM);
+  constexpr int kCrowdedBufs = DK == 128 ? 1 : 2;
+  return chains > st->sms
+             ? run(plain_kernel<DK, 32, kCrowdedBufs>, 4, chains,
+                   PlainCfg<DK, 32, kCrowdedBufs>::THREADS, PlainCfg<DK, 32, kCrowdedBufs>::SMEM)
+             : run(plain_kernel<DK, 32, 2>, 5, chains, PlainCfg<DK, 32, 2>::THREADS,
+                   PlainCfg<DK, 32, 2>::SMEM);
 }
 
 }  // namespace

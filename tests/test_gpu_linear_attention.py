@@ -404,9 +404,9 @@ def test_binding_refuses_a_workspace_elsewhere(nv):
         nv.linear_attention(*args, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
 
 
-@pytest.mark.parametrize("hv,dv", [(24, 128), (4, 64)])
+@pytest.mark.parametrize("hv,dv", [(24, 128), (12, 128), (4, 64)])
 @pytest.mark.parametrize("dk", [128, 64])
 @pytest.mark.parametrize("delta", [True, False])
 def test_long_sequences(nv, dk, hv, dv, delta):
-    """Many chunks in a row, with more CTAs of the chain than SMs and with fewer."""
+    """Many chunks in a row, with more chains than SMs, about as many, and few."""
     run_prompts(nv, [900, 1025], 2, hv, dk, dv, delta, True, dk + hv)

@@ -27,7 +27,7 @@
 // Measured: 8192 tokens, 16 key and 32 value heads of 128: prepare 96 us, chain
 // 330 us (128 steps of 2.5 us); 7777 tokens in 23 prompts, 48 value heads: 147
 // and 390 us under the profiler, 500 together; 4096 tokens in 3 prompts, 24 heads
-// of 64 x 128 without the delta rule: 22 and 70 us. All of them are bound by
+// of 64 x 128 without the delta rule: 20 and 70 us. All of them are bound by
 // latency, the chains by that of their dependent products.
 //
 // Precision: q, k, v are bf16 and enter the products exactly. FP32 operands are
@@ -647,7 +647,7 @@ constexpr int kCols = 16;                  // columns of d_v per compute thread
 // cycles from its issue to the arrival of its commit, so pieces in N cost less
 // than pieces one after the other. Compute threads hold one row, 16 columns
 // wide (the splitting stands on the critical path: 32 columns a thread took 400
-// cycles more per operand); one more warp loads and issues the MMAs.
+// cycles more per operand, 8 no fewer); one more warp loads and issues the MMAs.
 // (The kernel of the delta rule; the plain one is below.)
 // A step of one chunk is a chain of latencies (4.4 K cycles, 1.2 K of them in
 // MMAs), so two CTAs share an SM and fill each other's gaps; for that the

@@ -41,6 +41,8 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_sf_bytes", "nvfp4_quantize_workspace_by
            "nvfp4_linear_attention_step",
            "nvfp4_selftest_wait_timeout", "nvfp4_selftest_gemm_stall")
 
+_BF16, _FP32 = torch.bfloat16, torch.float32
+
 # activations of the GEMM epilogue (nvfp4_activation)
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
@@ -394,39 +396,44 @@ def silu_mul(y: torch.Tensor, out: torch.Tensor | None = None,
 
 def _heads(q, k, v, decay, beta, state, out):
     """Checked arguments shared by linear_attention and its step: (h_k, h_v,
-    d_k, d_v, row pitches of q, k, v and out, out)."""
+    d_k, d_v, row pitches of q, k, v and out, out). One condition per tensor, not
+    a loop over them: a call on one token waits for the host."""
     dev = q.get_device()
     if dev < 0:
         raise ValueError("q must be a CUDA tensor")
     if dev != torch.cuda.current_device():
         raise ValueError(f"q is on cuda:{dev}, the current device is {torch.cuda.current_device()}")
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != dev
-                              or t.dim() != 3):
-            raise ValueError(f"{name} must be {torch.bfloat16} [rows, heads, dim] on cuda:{dev}")
-    rows, hk, dk = qs = q.shape
-    vr, hv, dv = vs = v.shape
-    if k.shape != qs or vr != rows:
-        raise ValueError("q and k must be [rows, h_k, d_k], v [rows, h_v, d_v]")
-    for t, name, shape in ((decay, "decay", (rows, hv)), (beta, "beta", (rows, hv)),
-                           (state, "state", (hv, dk, dv))):
-        if t is None:
-            continue
-        if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {torch.float32} on cuda:{dev}")
-        if (t.shape[1:] if t is state else t.shape) != shape:
-            raise ValueError(f"{name} must be {'[slots] + ' if t is state else ''}{list(shape)}")
+    qs, vs = q.shape, v.shape
+    if (len(qs) != 3 or len(vs) != 3 or k.shape != qs or vs[0] != qs[0]
+            or not (q.dtype is k.dtype is v.dtype is _BF16)
+            or k.get_device() != dev or v.get_device() != dev):
+        raise ValueError(f"q and k must be [rows, h_k, d_k], v [rows, h_v, d_v], all {_BF16} on "
+                         f"cuda:{dev}")
+    rows, hk, dk = qs
+    _, hv, dv = vs
     if out is None:
-        out = torch.empty((rows, hv, dv), dtype=torch.bfloat16, device=q.device)
-    elif out.shape != vs:
-        raise ValueError(f"out must be [{rows}, {hv}, {dv}]")
-    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
-    if ((dk > 1 and (sq[2] != 1 or sk[2] != 1)) or (hk > 1 and (sq[1] != dk or sk[1] != dk))
-            or (dv > 1 and (sv[2] != 1 or so[2] != 1))
-            or (hv > 1 and (sv[1] != dv or so[1] != dv))):
+        out = torch.empty(vs, dtype=_BF16, device=q.device)
+    elif out.shape != vs or out.dtype is not _BF16 or out.get_device() != dev:
+        raise ValueError(f"out must be {_BF16} {list(vs)} on cuda:{dev}")
+    gates = (rows, hv)
+    if (decay.shape != gates or decay.dtype is not _FP32 or decay.get_device() != dev
+            or not decay.is_contiguous()):
+        raise ValueError(f"decay must be contiguous {_FP32} {list(gates)} on cuda:{dev}")
+    if beta is not None and (beta.shape != gates or beta.dtype is not _FP32
+                             or beta.get_device() != dev or not beta.is_contiguous()):
+        raise ValueError(f"beta must be contiguous {_FP32} {list(gates)} on cuda:{dev}")
+    if state is not None and (state.shape[1:] != (hv, dk, dv) or state.dtype is not _FP32
+                              or state.get_device() != dev or not state.is_contiguous()):
+        raise ValueError(f"state must be contiguous {_FP32} [slots] + {[hv, dk, dv]} on cuda:{dev}")
+    lq, hq, eq = q.stride()
+    lk, hk_, ek = k.stride()
+    lv, hv_, ev = v.stride()
+    lo, ho, eo = out.stride()
+    if ((dk > 1 and (eq != 1 or ek != 1)) or (hk > 1 and (hq != dk or hk_ != dk))
+            or (dv > 1 and (ev != 1 or eo != 1)) or (hv > 1 and (hv_ != dv or ho != dv))):
         raise ValueError("the heads of a row of q, k, v and out must be contiguous")
     if rows > 1:
-        return hk, hv, dk, dv, (sq[0], sk[0], sv[0], so[0]), out
+        return hk, hv, dk, dv, (lq, lk, lv, lo), out
     ldk, ldv = -(-hk * dk // 8) * 8, -(-hv * dv // 8) * 8  # a single row's pitch is free
     return hk, hv, dk, dv, (ldk, ldk, ldv, ldv), out
 

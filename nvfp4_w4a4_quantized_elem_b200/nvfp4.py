@@ -127,6 +127,35 @@ def _stream(stream: torch.cuda.Stream | None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+# Buffers that a call makes for itself belong to the stream its kernels run on:
+# made (or zero-filled) on the current stream, nothing would order the fill, or
+# what a recycled block still serves, before them. `stream` None is the current
+# stream. What is handed to the caller is recorded as used on the caller's
+# stream, so that its memory is not reused under work queued there. The inputs
+# are the caller's: ordered before `stream`, and kept until it has read them.
+def _on(stream: torch.cuda.Stream | None):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype: torch.dtype, device, stream: torch.cuda.Stream | None) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _given(t: torch.Tensor, stream: torch.cuda.Stream | None) -> torch.Tensor:
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _given_nvfp4(t: NVFP4Tensor, stream: torch.cuda.Stream | None) -> NVFP4Tensor:
+    for part in (t.codes, t.sf, t.global_scale):
+        _given(part, stream)
+    return t
+
+
 def _require_cuda(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> None:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -170,10 +199,11 @@ def quantize(x: torch.Tensor, global_scale: torch.Tensor | None = None,
         raise ValueError("x must be 2-D with unit stride along k")
     rows, k = x.shape
     if out is None:
-        out = NVFP4Tensor.empty(rows, k, x.device)
+        with _on(stream):
+            out = NVFP4Tensor.empty(rows, k, x.device)
+        _given_nvfp4(out, stream)
     if global_scale is None and workspace is None:
-        workspace = torch.empty(quantize_workspace_bytes(rows, k), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _empty(quantize_workspace_bytes(rows, k), torch.uint8, x.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().nvfp4_quantize(_ptr(x), rows, k, x.stride(0), _ptr(global_scale),
                               _ptr(out.codes), _ptr(out.sf), _ptr(out.global_scale),
@@ -207,7 +237,7 @@ class Calibrator:
     def __init__(self, device="cuda"):
         self.running_amax = torch.zeros(1, dtype=torch.float32, device=device)
         self.global_scale = torch.ones(1, dtype=torch.float32, device=device)
-        self._ws = None
+        self._ws = self._ws_stream = None
 
     def observe(self, x: torch.Tensor, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
         _require_cuda(x, "x", torch.bfloat16)
@@ -215,8 +245,9 @@ class Calibrator:
             raise ValueError("x must be 2-D with unit stride along k")
         rows, k = x.shape
         need = quantize_workspace_bytes(rows, k)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        if self._ws is None or self._ws.numel() < need or self._ws_stream != _stream(stream):
+            self._ws = _empty(need, torch.uint8, x.device, stream)
+            self._ws_stream = _stream(stream)
         st = lib().nvfp4_calibrate_global(_ptr(x), rows, k, x.stride(0), _ptr(self.running_amax),
                                           _ptr(self.global_scale), _ptr(self._ws), self._ws.numel(),
                                           _stream(stream))
@@ -266,7 +297,7 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out: torch.Tensor | None = None,
         raise ValueError("k mismatch")
     m, n, k = a.rows, b.rows, a.k
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=a.codes.device)
+        out = _given(_empty((m, n), out_dtype, a.codes.device, stream), stream)
     if out.dtype not in (torch.bfloat16, torch.float32) or out.stride(1) != 1:
         raise ValueError("out must be bf16/fp32 with unit column stride")
     y_dtype = 0 if out.dtype == torch.bfloat16 else 1
@@ -308,9 +339,13 @@ def gemm_swiglu_quant(a: NVFP4Tensor, b_interleaved: NVFP4Tensor, h_global: torc
     if a.k != b_interleaved.k:
         raise ValueError("k mismatch")
     m, ffn, k = a.rows, b_interleaved.rows // 2, a.k
-    if out is None:
-        out = NVFP4Tensor.empty(m, ffn, a.codes.device)
-    out.global_scale.copy_(h_global.reshape(1))
+    made = out is None
+    with _on(stream):
+        if made:
+            out = NVFP4Tensor.empty(m, ffn, a.codes.device)
+        out.global_scale.copy_(h_global.reshape(1))
+    if made:
+        _given_nvfp4(out, stream)
     st = lib().nvfp4_gemm_swiglu_quant(_ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale),
                                        _ptr(b_interleaved.codes), _ptr(b_interleaved.sf),
                                        _ptr(b_interleaved.global_scale), _ptr(h_global),
@@ -336,10 +371,14 @@ def gemm_swiglu_quant_dynamic(a: NVFP4Tensor, b_interleaved: NVFP4Tensor,
     if a.k != b_interleaved.k:
         raise ValueError("k mismatch")
     m, ffn, k = a.rows, b_interleaved.rows // 2, a.k
-    if out is None:
-        out = NVFP4Tensor.empty(m, ffn, a.codes.device)
-    if workspace is None:
-        workspace = swiglu_quant_dynamic_workspace(m, ffn, a.codes.device)
+    made = out is None
+    with _on(stream):
+        if made:
+            out = NVFP4Tensor.empty(m, ffn, a.codes.device)
+        if workspace is None:
+            workspace = swiglu_quant_dynamic_workspace(m, ffn, a.codes.device)
+    if made:
+        _given_nvfp4(out, stream)
     st = lib().nvfp4_gemm_swiglu_quant_dynamic(
         _ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale), _ptr(b_interleaved.codes),
         _ptr(b_interleaved.sf), _ptr(b_interleaved.global_scale), _ptr(out.codes), _ptr(out.sf),
@@ -360,10 +399,11 @@ def fuse_group_scales(modules: list[NVFP4Tensor], sf_out: torch.Tensor | None = 
     total = sum(m.rows for m in modules)
     dev = modules[0].codes.device
     if sf_out is None:
-        sf_out = torch.empty(sf_bytes(total, k), dtype=torch.uint8, device=dev)
+        sf_out = _given(_empty(sf_bytes(total, k), torch.uint8, dev, stream), stream)
     if global_out is None:
-        global_out = torch.empty(1, dtype=torch.float32, device=dev)
-    globals_in = torch.cat([m.global_scale for m in modules])
+        global_out = _given(_empty(1, torch.float32, dev, stream), stream)
+    with _on(stream):
+        globals_in = torch.cat([m.global_scale for m in modules])
     rows = (ctypes.c_int64 * n)(*[m.rows for m in modules])
     ptrs = (ctypes.c_void_p * n)(*[m.sf.data_ptr() for m in modules])
     st = lib().nvfp4_fuse_group_scales(n, ctypes.cast(rows, ctypes.c_void_p), k,
@@ -376,7 +416,9 @@ def fuse_group_scales(modules: list[NVFP4Tensor], sf_out: torch.Tensor | None = 
 def fuse_group(modules: list[NVFP4Tensor], stream=None) -> NVFP4Tensor:
     """The repaired fused tensor: concatenated codes, folded scales, g*."""
     sf, g = fuse_group_scales(modules, stream=stream)
-    codes = torch.cat([m.codes for m in modules], dim=0)
+    with _on(stream):
+        codes = torch.cat([m.codes for m in modules], dim=0)
+    _given(codes, stream)
     return NVFP4Tensor(codes, sf, g, codes.shape[0], modules[0].k)
 
 
@@ -387,14 +429,14 @@ def silu_mul(y: torch.Tensor, out: torch.Tensor | None = None,
     m, n2 = y.shape
     n = n2 // 2
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=y.device)
+        out = _given(_empty((m, n), torch.bfloat16, y.device, stream), stream)
     st = lib().nvfp4_silu_mul(_ptr(y), m, n, y.stride(0), _ptr(out), out.stride(0),
                               _stream(stream))
     _check(st, "nvfp4_silu_mul")
     return out
 
 
-def _heads(q, k, v, decay, beta, state, out):
+def _heads(q, k, v, decay, beta, state, out, stream):
     """Checked arguments shared by linear_attention and its step: (h_k, h_v,
     d_k, d_v, row pitches of q, k, v and out, out). One condition per tensor, not
     a loop over them: a call on one token waits for the host."""
@@ -412,7 +454,7 @@ def _heads(q, k, v, decay, beta, state, out):
     rows, hk, dk = qs
     _, hv, dv = vs
     if out is None:
-        out = torch.empty(vs, dtype=_BF16, device=q.device)
+        out = _given(_empty(vs, _BF16, q.device, stream), stream)
     elif out.shape != vs or out.dtype is not _BF16 or out.get_device() != dev:
         raise ValueError(f"out must be {_BF16} {list(vs)} on cuda:{dev}")
     gates = (rows, hv)
@@ -462,8 +504,8 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
     states go to ``state`` FP32 [slots, h_v, d_k, d_v] at ``slots`` (int32
     [n_seq], None: in order), and come from there where ``resume`` (int32
     [n_seq]) is nonzero. ``scale`` defaults to d_k ** -0.5. The workspace is
-    allocated on ``stream`` when None."""
-    hk, hv, dk, dv, (ldq, ldk, ldv, ldo), out = _heads(q, k, v, decay, beta, state, out)
+    allocated here when None."""
+    hk, hv, dk, dv, (ldq, ldk, ldv, ldo), out = _heads(q, k, v, decay, beta, state, out, stream)
     total = q.shape[0]
     n_seq = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
     _int32(cu_seqlens, "cu_seqlens", n_seq + 1, q.device)
@@ -471,8 +513,7 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
     _int32(resume, "resume", n_seq, q.device)
     if workspace is None:
         need = linear_attention_workspace_bytes(total, n_seq, hk, hv, dk)
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     elif workspace.device != q.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {q.device}")
     st = lib().nvfp4_linear_attention(
@@ -492,7 +533,7 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dec
     """nvfp4_linear_attention_step: one token per row, states updated in place.
     Shapes as linear_attention with rows = batch; ``slots`` int32 [batch] (None:
     row i uses slot i), a slot outside the pool marks a padding row."""
-    hk, hv, dk, dv, (ldq, ldk, ldv, ldo), out = _heads(q, k, v, decay, beta, state, out)
+    hk, hv, dk, dv, (ldq, ldk, ldv, ldo), out = _heads(q, k, v, decay, beta, state, out, stream)
     batch = q.shape[0]
     _int32(slots, "slots", batch, q.device)
     st = lib().nvfp4_linear_attention_step(
@@ -528,7 +569,7 @@ def selftest_gemm_stall(a: NVFP4Tensor, b: NVFP4Tensor, limit_ns: int = 1_000_00
     ``limit_ns``; the kernel gives up and returns (read_fault() then returns
     the role bits that timed out)."""
     m, n, k = a.rows, b.rows, a.k
-    y = torch.empty((m, n), dtype=torch.bfloat16, device=a.codes.device)
+    y = _empty((m, n), torch.bfloat16, a.codes.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().nvfp4_selftest_gemm_stall(_ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale),
                                            _ptr(b.codes), _ptr(b.sf), _ptr(b.global_scale),
@@ -567,11 +608,12 @@ def linear(x: torch.Tensor, w: NVFP4Tensor, out: torch.Tensor | None = None,
         raise ValueError("k mismatch")
     n = w.rows
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        out = _given(_empty((m, n), out_dtype, x.device, stream), stream)
     if out.dtype not in (torch.bfloat16, torch.float32) or out.stride(1) != 1:
         raise ValueError("out must be bf16/fp32 with unit column stride")
     if workspace is None:
-        workspace = linear_workspace(m, n, k, x.device)
+        with _on(stream):
+            workspace = linear_workspace(m, n, k, x.device)
     if bias is not None or residual is not None or activation != "none":
         st = lib().nvfp4_linear_epilogue(
             _ptr(x), m, k, x.stride(0), _ptr(global_scale), _ptr(w.codes), _ptr(w.sf),

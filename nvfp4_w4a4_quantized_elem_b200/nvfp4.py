@@ -163,6 +163,31 @@ def _require_cuda(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) 
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _scratch(workspace: torch.Tensor | None, dev: int) -> tuple[int | None, int]:
+    """Pointer and bytes of a caller's workspace on cuda:``dev``."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _global(g: torch.Tensor | None, name: str, dev: int) -> int | None:
+    """Pointer of a global scale on cuda:``dev``."""
+    if g is None:
+        return None
+    if g.get_device() != dev or g.dtype is not _FP32 or g.numel() < 1:
+        raise ValueError(f"{name} must be a {_FP32} element on cuda:{dev}")
+    return g.data_ptr()
+
+
+def _operand(t: NVFP4Tensor, name: str, dev: int) -> tuple[int, int, int]:
+    """Pointers of codes, scales and global of an operand on cuda:``dev``."""
+    if dev < 0 or t.codes.get_device() != dev or t.sf.get_device() != dev:
+        raise ValueError(f"{name} must be on the CUDA device of the call's other tensors")
+    return t.codes.data_ptr(), t.sf.data_ptr(), _global(t.global_scale, f"{name}'s global", dev)
+
+
 def sf_bytes(rows: int, k: int) -> int:
     return int(lib().nvfp4_sf_bytes(rows, k))
 
@@ -204,10 +229,11 @@ def quantize(x: torch.Tensor, global_scale: torch.Tensor | None = None,
         _given_nvfp4(out, stream)
     if global_scale is None and workspace is None:
         workspace = _empty(quantize_workspace_bytes(rows, k), torch.uint8, x.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().nvfp4_quantize(_ptr(x), rows, k, x.stride(0), _ptr(global_scale),
-                              _ptr(out.codes), _ptr(out.sf), _ptr(out.global_scale),
-                              _ptr(workspace), ws_bytes, _stream(stream))
+    dev = x.get_device()
+    st = lib().nvfp4_quantize(_ptr(x), rows, k, x.stride(0),
+                              _global(global_scale, "global_scale", dev),
+                              *_operand(out, "out", dev), *_scratch(workspace, dev),
+                              _stream(stream))
     _check(st, "nvfp4_quantize")
     return out
 
@@ -222,9 +248,10 @@ def quantize_noalloc(x: torch.Tensor, out: NVFP4Tensor, global_scale: torch.Tens
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit stride along k")
     rows, k = x.shape
-    st = lib().nvfp4_quantize_noalloc(_ptr(x), rows, k, x.stride(0), _ptr(global_scale),
-                                      _ptr(out.codes), _ptr(out.sf), _ptr(out.global_scale),
-                                      _stream(stream))
+    dev = x.get_device()
+    st = lib().nvfp4_quantize_noalloc(_ptr(x), rows, k, x.stride(0),
+                                      _global(global_scale, "global_scale", dev),
+                                      *_operand(out, "out", dev), _stream(stream))
     _check(st, "nvfp4_quantize_noalloc")
     return out
 
@@ -255,12 +282,19 @@ class Calibrator:
         return self.global_scale
 
 
+def _product(out: torch.Tensor, m: int, n: int, dev: int) -> tuple[int, int, int]:
+    """Checked [m, n] output of a product on cuda:``dev``: pointer, type, row pitch."""
+    if out.dtype not in (_BF16, _FP32) or out.shape != (m, n) or out.stride(1) != 1:
+        raise ValueError(f"out must be bf16/fp32 [{m}, {n}] with unit column stride")
+    if out.get_device() != dev:
+        raise ValueError(f"out must be on cuda:{dev}")
+    return out.data_ptr(), 0 if out.dtype is _BF16 else 1, out.stride(0)
+
+
 def _epilogue(bias: torch.Tensor | None, activation: str, residual: torch.Tensor | None,
-              m: int, n: int, out: torch.Tensor, device: torch.device):
+              m: int, n: int, device: torch.device):
     """Checked epilogue arguments: (bias pointer, activation code, residual
     pointer, residual row pitch)."""
-    if tuple(out.shape) != (m, n) or out.device != device:
-        raise ValueError(f"out must be [{m}, {n}] on {device}")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
     for t, name in ((bias, "bias"), (residual, "residual")):
@@ -298,22 +332,17 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out: torch.Tensor | None = None,
     m, n, k = a.rows, b.rows, a.k
     if out is None:
         out = _given(_empty((m, n), out_dtype, a.codes.device, stream), stream)
-    if out.dtype not in (torch.bfloat16, torch.float32) or out.stride(1) != 1:
-        raise ValueError("out must be bf16/fp32 with unit column stride")
-    y_dtype = 0 if out.dtype == torch.bfloat16 else 1
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    dev = a.codes.get_device()
+    y = _product(out, m, n, dev)
+    operands = (*_operand(a, "a", dev), *_operand(b, "b", dev))
+    ws, ws_bytes = _scratch(workspace, dev)
     if bias is not None or residual is not None or activation != "none":
         st = lib().nvfp4_gemm_epilogue(
-            _ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale), _ptr(b.codes), _ptr(b.sf),
-            _ptr(b.global_scale), *_epilogue(bias, activation, residual, m, n, out, a.codes.device),
-            _ptr(out), y_dtype, out.stride(0), m, n, k, _ptr(workspace), ws_bytes,
-            _stream(stream))
+            *operands, *_epilogue(bias, activation, residual, m, n, a.codes.device), *y, m, n, k,
+            ws, ws_bytes, _stream(stream))
         _check(st, "nvfp4_gemm_epilogue")
         return out
-    st = lib().nvfp4_gemm(_ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale),
-                          _ptr(b.codes), _ptr(b.sf), _ptr(b.global_scale),
-                          _ptr(out), y_dtype, out.stride(0), m, n, k, _ptr(workspace), ws_bytes,
-                          _stream(stream))
+    st = lib().nvfp4_gemm(*operands, *y, m, n, k, ws, ws_bytes, _stream(stream))
     _check(st, "nvfp4_gemm")
     return out
 
@@ -339,6 +368,8 @@ def gemm_swiglu_quant(a: NVFP4Tensor, b_interleaved: NVFP4Tensor, h_global: torc
     if a.k != b_interleaved.k:
         raise ValueError("k mismatch")
     m, ffn, k = a.rows, b_interleaved.rows // 2, a.k
+    dev = a.codes.get_device()
+    h_ptr = _global(h_global, "h_global", dev)
     made = out is None
     with _on(stream):
         if made:
@@ -346,10 +377,9 @@ def gemm_swiglu_quant(a: NVFP4Tensor, b_interleaved: NVFP4Tensor, h_global: torc
         out.global_scale.copy_(h_global.reshape(1))
     if made:
         _given_nvfp4(out, stream)
-    st = lib().nvfp4_gemm_swiglu_quant(_ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale),
-                                       _ptr(b_interleaved.codes), _ptr(b_interleaved.sf),
-                                       _ptr(b_interleaved.global_scale), _ptr(h_global),
-                                       _ptr(out.codes), _ptr(out.sf), m, ffn, k, _stream(stream))
+    st = lib().nvfp4_gemm_swiglu_quant(*_operand(a, "a", dev),
+                                       *_operand(b_interleaved, "b_interleaved", dev), h_ptr,
+                                       *_operand(out, "out", dev)[:2], m, ffn, k, _stream(stream))
     _check(st, "nvfp4_gemm_swiglu_quant")
     return out
 
@@ -379,11 +409,10 @@ def gemm_swiglu_quant_dynamic(a: NVFP4Tensor, b_interleaved: NVFP4Tensor,
             workspace = swiglu_quant_dynamic_workspace(m, ffn, a.codes.device)
     if made:
         _given_nvfp4(out, stream)
+    dev = a.codes.get_device()
     st = lib().nvfp4_gemm_swiglu_quant_dynamic(
-        _ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale), _ptr(b_interleaved.codes),
-        _ptr(b_interleaved.sf), _ptr(b_interleaved.global_scale), _ptr(out.codes), _ptr(out.sf),
-        _ptr(out.global_scale), m, ffn, k, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        *_operand(a, "a", dev), *_operand(b_interleaved, "b_interleaved", dev),
+        *_operand(out, "out", dev), m, ffn, k, *_scratch(workspace, dev), _stream(stream))
     _check(st, "nvfp4_gemm_swiglu_quant_dynamic")
     return out
 
@@ -514,13 +543,11 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
     if workspace is None:
         need = linear_attention_workspace_bytes(total, n_seq, hk, hv, dk)
         workspace = _empty(need, torch.uint8, q.device, stream)
-    elif workspace.device != q.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {q.device}")
     st = lib().nvfp4_linear_attention(
         _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(decay), _ptr(beta),
         dk ** -0.5 if scale is None else scale, total, hk, hv, dk, dv, n_seq, _ptr(cu_seqlens),
         _ptr(state), 0 if state is None else state.shape[0], _ptr(slots), _ptr(resume), _ptr(out),
-        ldo, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        ldo, *_scratch(workspace, q.get_device()), _stream(stream))
     _check(st, "nvfp4_linear_attention")
     return out
 
@@ -570,10 +597,9 @@ def selftest_gemm_stall(a: NVFP4Tensor, b: NVFP4Tensor, limit_ns: int = 1_000_00
     the role bits that timed out)."""
     m, n, k = a.rows, b.rows, a.k
     y = _empty((m, n), torch.bfloat16, a.codes.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().nvfp4_selftest_gemm_stall(_ptr(a.codes), _ptr(a.sf), _ptr(a.global_scale),
-                                           _ptr(b.codes), _ptr(b.sf), _ptr(b.global_scale),
-                                           _ptr(y), m, n, k, limit_ns, _ptr(workspace), ws_bytes,
+    dev = a.codes.get_device()
+    _check(lib().nvfp4_selftest_gemm_stall(*_operand(a, "a", dev), *_operand(b, "b", dev),
+                                           _ptr(y), m, n, k, limit_ns, *_scratch(workspace, dev),
                                            _stream(stream)),
            "nvfp4_selftest_gemm_stall")
 
@@ -609,23 +635,20 @@ def linear(x: torch.Tensor, w: NVFP4Tensor, out: torch.Tensor | None = None,
     n = w.rows
     if out is None:
         out = _given(_empty((m, n), out_dtype, x.device, stream), stream)
-    if out.dtype not in (torch.bfloat16, torch.float32) or out.stride(1) != 1:
-        raise ValueError("out must be bf16/fp32 with unit column stride")
+    dev = x.get_device()
+    y = _product(out, m, n, dev)
     if workspace is None:
         with _on(stream):
             workspace = linear_workspace(m, n, k, x.device)
+    args = (_ptr(x), m, k, x.stride(0), _global(global_scale, "global_scale", dev),
+            *_operand(w, "w", dev), n)
+    ws, ws_bytes = _scratch(workspace, dev)
     if bias is not None or residual is not None or activation != "none":
         st = lib().nvfp4_linear_epilogue(
-            _ptr(x), m, k, x.stride(0), _ptr(global_scale), _ptr(w.codes), _ptr(w.sf),
-            _ptr(w.global_scale), n, *_epilogue(bias, activation, residual, m, n, out, x.device),
-            _ptr(out), 0 if out.dtype == torch.bfloat16 else 1, out.stride(0), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream))
+            *args, *_epilogue(bias, activation, residual, m, n, x.device), *y, ws, ws_bytes,
+            _stream(stream))
         _check(st, "nvfp4_linear_epilogue")
         return out
-    st = lib().nvfp4_linear(_ptr(x), m, k, x.stride(0), _ptr(global_scale), _ptr(w.codes),
-                            _ptr(w.sf), _ptr(w.global_scale), n, _ptr(out),
-                            0 if out.dtype == torch.bfloat16 else 1, out.stride(0),
-                            _ptr(workspace), workspace.numel() * workspace.element_size(),
-                            _stream(stream))
+    st = lib().nvfp4_linear(*args, *y, ws, ws_bytes, _stream(stream))
     _check(st, "nvfp4_linear")
     return out

@@ -496,6 +496,10 @@ size_t nvfp4_linear_attention_workspace_bytes(int64_t total, int64_t n_seq, int 
  * A NaN or an infinity in a token's inputs reaches the later tokens of its
  * sequence, as in the formula, and also the earlier ones of its 64-token chunk
  * (their zero factors multiply it); other sequences and heads stay clean.
+ * A wait that runs out (nvfp4_read_fault: bit 512 the first kernel, 1024 and
+ * 2048 the second) ends its head of its sequence: the state stays as it was, in
+ * the second kernel that of the CTA's columns of d_v, and the rows of o are left
+ * undefined.
  * Errors: INVALID_ARG, UNSUPPORTED (d_k, d_v, sizes >= 2^31), MISALIGNED, CUDA.
  */
 nvfp4_status nvfp4_linear_attention(const void* q, int64_t ldq, const void* k, int64_t ldk,
@@ -552,6 +556,26 @@ nvfp4_status nvfp4_selftest_gemm_stall(const uint8_t* a_codes, const uint8_t* a_
                                        int64_t m, int64_t n, int64_t k, uint64_t limit_ns,
                                        void* workspace, size_t workspace_bytes,
                                        nvfp4_stream_t stream);
+
+/*
+ * nvfp4_selftest_linear_attention_stall — the same for the two kernels of
+ * nvfp4_linear_attention: CTA `cta` of the first (`kernel` 0: one per 64-token
+ * chunk slot and value head, heads fastest) never issues its first product, or
+ * CTA `cta` of the second (`kernel` 1: one per sequence, head and 16 or 32
+ * columns of d_v, columns fastest) never asks for its first keys, and every
+ * wait is limited to limit_ns. nvfp4_read_fault then reports bit 512, or 1024
+ * and / or 2048. Head and sequence of that CTA: the state stays as it was (of
+ * its columns, for kernel 1), the rows of o are left undefined; the others get
+ * their results. A `cta` outside the grid stalls nothing.
+ *   Arguments as nvfp4_linear_attention; limit_ns in [1 us, 10 s].
+ * Errors: as nvfp4_linear_attention; INVALID_ARG for the last three.
+ */
+nvfp4_status nvfp4_selftest_linear_attention_stall(
+    const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+    const float* decay, const float* beta, float scale, int64_t total, int h_k, int h_v, int d_k,
+    int d_v, int64_t n_seq, const int32_t* cu_seqlens, float* state, int64_t n_slots,
+    const int32_t* slots, const int32_t* resume, void* o, int64_t ldo, void* workspace,
+    size_t workspace_bytes, int kernel, int cta, uint64_t limit_ns, nvfp4_stream_t stream);
 
 /*
  * nvfp4_read_fault — every mbarrier wait in the GEMM and linear-attention

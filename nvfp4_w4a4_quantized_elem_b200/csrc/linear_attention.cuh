@@ -52,9 +52,9 @@ namespace la {
 constexpr int C = 64;                       // tokens per chunk
 constexpr int kHalfBytes = 128 * 128;       // [K; Q] image: 128 rows x 64 of d_k
 constexpr int kTTBytes = 128 * 128;         // [T; AT] image: 128 rows x 64, one piece
-constexpr int kGateFloats = 3 * C + 4;      // e^G, e^{G_64 - G}, beta, e^{G_64}
+constexpr int kGateFloats = 3 * C + 4;      // e^G, e^{G_64 - G}, beta; e^{G_64}, valid word
 constexpr int kGateBytes = (kGateFloats * 4 + 127) / 128 * 128;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // per wait, unless a self-test sets less
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 
 enum : uint32_t { kFaultPrepare = 512u, kFaultChainMma = 1024u, kFaultChain = 2048u };
@@ -79,6 +79,10 @@ struct Args {
   __nv_bfloat16* o;         // [total][ldo]
   uint8_t* kq;              // [chunk slots][h_k] images
   uint8_t* tt;              // [chunk slots][h_v] images and gates
+  uint64_t wait_limit_ns;
+  // self-test: the CTA of the first or the second kernel whose first product or
+  // first load is never issued (-1: none)
+  int stall_prepare, stall_chain;
 };
 
 // Sequence b's tokens [start, end): offsets outside [0, total] or decreasing
@@ -199,16 +203,17 @@ __device__ __forceinline__ void tc_ld(uint32_t taddr, float (&x)[N]) {
 }
 
 // The slow part of a wait, out of line: many tries between two looks at the
-// clock, at most 2 s.
+// clock, up to the limit.
 __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity,
-                                       volatile uint32_t* abort_flag, uint32_t who) {
+                                       volatile uint32_t* abort_flag, uint32_t who,
+                                       uint64_t limit_ns) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (ptx::mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+    if (ptx::globaltimer_ns() - t0 > limit_ns) {
       *abort_flag = 1u;
       atomicOr(&g_fault_word, who);
       return false;
@@ -219,8 +224,9 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity,
 // Bounded wait: one try in line, the rest out of line (the waits of the chain
 // are short and stand one behind the other).
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
-                                             volatile uint32_t* abort_flag, uint32_t who) {
-  return ptx::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, who);
+                                             volatile uint32_t* abort_flag, uint32_t who,
+                                             uint64_t limit_ns) {
+  return ptx::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, who, limit_ns);
 }
 
 // Used only while aborting: wait for in-flight asynchronous work, bounded.
@@ -232,8 +238,9 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
-                                          volatile uint32_t* abort_flag, uint32_t who) {
-  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, who));
+                                          volatile uint32_t* abort_flag, uint32_t who,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, who, limit_ns));
 }
 
 // ------------------------------------------------------------------ prepare --
@@ -406,12 +413,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bar + 1);
   volatile uint32_t* const abort_flag = tmem_holder + 1;
   int2* const found = reinterpret_cast<int2*>(bar + 2);  // the chunk's first token, its tokens
+  uint64_t* const drain = bar + 3;
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int h = blockIdx.x % a.h_v, group = a.h_v / a.h_k, hk = h / group;
   const int slot = blockIdx.x / a.h_v;
   if (t == 0) {
     ptx::mbar_init(bar, 1);
+    ptx::mbar_init(drain, 1);
     *found = make_int2(0, 0);
     // the swizzled images need the alignment that the declaration asks for
     *abort_flag = (ptx::smem_u32(smem) & 1023u) != 0u ? 1u : 0u;
@@ -507,7 +516,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   const uint32_t tmem = *tmem_holder;
   const uint32_t sb = ptx::smem_u32(smem);
   bool ok = *abort_flag == 0u;
-  if (t == 0 && ok) {
+  if (t == 0 && ok && a.stall_prepare != static_cast<int>(blockIdx.x)) {
     // [K; Q] K^T: 128 x 64
     constexpr uint32_t kScores = ptx::idesc_bf16(128, C, false, false);
 #pragma unroll
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     }
     ptx::tc_commit(bar);
   }
-  ok = ok && warp_wait(bar, 0, abort_flag, kFaultPrepare);
+  ok = ok && warp_wait(bar, 0, abort_flag, kFaultPrepare, a.wait_limit_ns);
   ptx::tc_fence_after();
   __syncthreads();  // every warp saw the scores: L may go over their operands
   // this thread: row r of the 128 (a token's row of L and T, then of A and AT),
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                            p == 0 ? kBoth : kOne, (p | s) != 0);
       ptx::tc_commit(bar);
     }
-    ok = ok && warp_wait(bar, 1, abort_flag, kFaultPrepare);
+    ok = ok && warp_wait(bar, 1, abort_flag, kFaultPrepare, a.wait_limit_ns);
     ptx::tc_fence_after();
     if (r >= C && !above) {
       float y[32];
@@ -621,14 +630,24 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();
+  // A CTA that gave up says so to the chains, which then leave their states
+  // alone, and lets its products end before their tensor memory goes.
+  const bool failed = *abort_flag != 0u;  // (not written behind the barrier above)
   if (t == 0) {
-    const int skip = delta ? 0 : kTTBytes / 2;
-    ptx::bulk_store(out + skip, smem + P::T_OFF + skip, kTTBytes - skip);
-    ptx::bulk_store(out + kTTBytes + skip, smem + P::L_OFF + skip, kTTBytes - skip);
-    ptx::bulk_commit_group();
-    // (the grid's end waits for the writes; the CTA only for its shared memory)
-    ptx::bulk_wait_group_read<0>();
+    reinterpret_cast<uint32_t*>(out + 2 * kTTBytes)[3 * C + 1] = failed ? 0u : 1u;
+    if (failed) {
+      ptx::tc_commit(drain);
+      drain_wait(drain, 0);
+    } else {
+      const int skip = delta ? 0 : kTTBytes / 2;
+      ptx::bulk_store(out + skip, smem + P::T_OFF + skip, kTTBytes - skip);
+      ptx::bulk_store(out + kTTBytes + skip, smem + P::L_OFF + skip, kTTBytes - skip);
+      ptx::bulk_commit_group();
+      // (the grid's end waits for the writes; the CTA only for its shared memory)
+      ptx::bulk_wait_group_read<0>();
+    }
   }
+  if (failed) __syncthreads();
   ptx::tc_fence_after();
   if (warp == 1) {
     __syncwarp();
@@ -706,6 +725,14 @@ __device__ __forceinline__ void store_state(float* row, const float (&S)[kCols])
 #pragma unroll
   for (int j = 0; j < kCols / 4; ++j)
     reinterpret_cast<float4*>(row)[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+}
+
+// Whether prepare_kernel finished the chunk with this word (the same for the
+// whole CTA); if not, the CTA's other warps are told to stop.
+__device__ __forceinline__ bool prepared(float word, volatile uint32_t* abort_flag) {
+  if (__float_as_uint(word) == 1u) return true;
+  *abort_flag = 1u;
+  return false;
 }
 
 // o = scale (e^G (Q S) + A U), 16 columns of one token.
@@ -817,16 +844,16 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
       int kq_asked = 0, kq_seen = 0, tt_asked = 0, tt_seen = 0;  // chunks
       bool ok = *abort_flag == 0u;
       if (n > 0 && ok) {
-        load_kq(kq_asked++);
+        if (a.stall_chain != static_cast<int>(blockIdx.x)) load_kq(kq_asked++);
         load_tt(tt_asked++);
       }
       for (int c = 0; c < n && ok; ++c) {
         const uint32_t par = c & 1;
         const uint32_t kq = sb + par * kq_bytes(DK);
-        ok = wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma);
+        ok = wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         ++kq_seen;
-        ok = wait_bounded(s_ready, par, abort_flag, kFaultChainMma);
+        ok = wait_bounded(s_ready, par, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
@@ -837,10 +864,10 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
         // S in place means that the previous chunk's products, the last
         // readers of the other buffer, are complete
         if (c + 1 < n) load_kq(kq_asked++);
-        ok = wait_bounded(full_tt, par, abort_flag, kFaultChainMma);
+        ok = wait_bounded(full_tt, par, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         ++tt_seen;
-        ok = wait_bounded(x_ready, par, abort_flag, kFaultChainMma);
+        ok = wait_bounded(x_ready, par, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
@@ -851,7 +878,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
                              ptx::smem_desc(r + s * 256, 128, kXN, 0), p == 0 ? kI2 : kI2lo,
                              (p | s) != 0);
         ptx::tc_commit(d2);
-        ok = wait_bounded(u_ready, par, abort_flag, kFaultChainMma);
+        ok = wait_bounded(u_ready, par, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
@@ -883,7 +910,8 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
     float S[kCols];
     load_state(a, slot >= 0 && k_row < DK, b, state, S);
     // what the next chunk needs from memory, requested a chunk ahead
-    float eg = 0.0f, erest = 0.0f, bt = 0.0f, eall = 0.0f;
+    float eg = 0.0f, erest = 0.0f, bt = 0.0f;
+    float2 all = make_float2(0.0f, 0.0f);   // e^{G_64}; the word that says the chunk was prepared
     uint4 v[kCols / 8];
     auto fetch = [&](int c) {
       const int64_t tok = start + static_cast<int64_t>(c) * C + row;
@@ -892,7 +920,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
       eg = gate[row];
       erest = gate[C + row];
       bt = gate[2 * C + row];
-      eall = gate[3 * C];
+      all = *reinterpret_cast<const float2*>(gate + 3 * C);
 #pragma unroll
       for (int u = 0; u < kCols / 8; ++u) {
         v[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -914,12 +942,13 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
     if (n > 0) fetch(0);
     for (int c = 0; c < n; ++c) {
       const uint32_t par = c & 1;
+      if (!(ok = prepared(all.y, abort_flag))) break;
       if (DK == 128 || k_row < DK) store_row_split<kSPieces>(r_s, P::S_PIECE, k_row, DK * 16, S);
       publish(s_ready);
       const int64_t tok = start + static_cast<int64_t>(c) * C + row;
-      const float eg_c = eg, erest_c = erest, eall_c = eall;
+      const float eg_c = eg, erest_c = erest, eall_c = all.x;
       float D[kCols], Q[kCols];
-      if (!(ok = warp_wait(d1, par, abort_flag, kFaultChain))) break;
+      if (!(ok = warp_wait(d1, par, abort_flag, kFaultChain, a.wait_limit_ns))) break;
       ptx::tc_fence_after();
       ld_sum<kSPieces, DVB>(lanes, Q);
       if (is_k) {
@@ -940,7 +969,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
         arrive(x_ready);  // Q S is taken: the product after next may go over it
       }
       if (c + 1 < n) fetch(c + 1);
-      if (!(ok = warp_wait(d2, par, abort_flag, kFaultChain))) break;
+      if (!(ok = warp_wait(d2, par, abort_flag, kFaultChain, a.wait_limit_ns))) break;
       ptx::tc_fence_after();
       ld_sum<kPieces, DVB>(lanes + P::D2_COL, D);
       if (is_k) {
@@ -951,7 +980,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
       } else if (tok < end) {
         store_out(a.o + tok * a.ldo + col, a.scale, eg_c, Q, D);
       }
-      if (!(ok = warp_wait(d3, par, abort_flag, kFaultChain))) break;
+      if (!(ok = warp_wait(d3, par, abort_flag, kFaultChain, a.wait_limit_ns))) break;
       ptx::tc_fence_after();
       ld_sum<kPieces, DVB>(lanes, D);
 #pragma unroll
@@ -1084,16 +1113,16 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
       int kq_asked = 0, kq_seen = 0, a_asked = 0, a_seen = 0;  // chunks
       bool ok = *abort_flag == 0u;
       if (n > 0 && ok) {
-        load_kq(kq_asked++);
+        if (a.stall_chain != static_cast<int>(blockIdx.x)) load_kq(kq_asked++);
         load_a(a_asked++);
       }
       for (int c = 0; c < n && ok; ++c) {
         const uint32_t par = c & 1;
         const uint32_t kq = sb + par * kq_bytes(DK);
-        ok = wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma);
+        ok = wait_bounded(&full[par], (c >> 1) & 1, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         ++kq_seen;
-        ok = wait_bounded(v_ready, par, abort_flag, kFaultChainMma);
+        ok = wait_bounded(v_ready, par, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
@@ -1103,7 +1132,7 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
                            ptx::smem_desc(sb + P::U_OFF + s * 256, 128, kXN, 0), kI3, s != 0);
         ptx::tc_commit(d3);
         const uint32_t pieces = sb + P::A_OFF + c % A_BUFS * 2 * P::A_BYTES;
-        ok = wait_bounded(&full_a[c % A_BUFS], (c / A_BUFS) & 1, abort_flag, kFaultChainMma);
+        ok = wait_bounded(&full_a[c % A_BUFS], (c / A_BUFS) & 1, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         ++a_seen;
 #pragma unroll
@@ -1114,7 +1143,7 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
                              ptx::smem_desc(pieces + (p - 1) * P::A_BYTES + s * 32, 16, 1024, 2),
                              ptx::smem_desc(sb + P::V_OFF + s * 256, 128, kXN, 0), kI2, (p | s) != 0);
         ptx::tc_commit(d2);
-        ok = wait_bounded(s_ready, par, abort_flag, kFaultChainMma);
+        ok = wait_bounded(s_ready, par, abort_flag, kFaultChainMma, a.wait_limit_ns);
         if (!ok) break;
         // S in place: Q S of the chunk before is taken, and with it the last
         // reader of the other buffers complete
@@ -1127,7 +1156,7 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
                            ptx::smem_desc(sb + P::S_OFF + s * 256, 128, kSN, 0), kI1, s != 0);
         ptx::tc_commit(d1);
         if (A_BUFS == 1 && c + 1 < n) {
-          ok = wait_bounded(d2, par, abort_flag, kFaultChainMma);
+          ok = wait_bounded(d2, par, abort_flag, kFaultChainMma, a.wait_limit_ns);
           if (!ok) break;
           load_a(a_asked++);
         }
@@ -1154,14 +1183,15 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
     float S[kCols];
     load_state(a, slot >= 0 && k_row < DK, b, state, S);
     // what the next chunk needs from memory, requested a chunk ahead
-    float gate = 0.0f, eall = 0.0f;   // e^{G_64 - G} of rows of V, e^G of rows of Q; e^{G_64}
+    float gate = 0.0f;   // e^{G_64 - G} of rows of V, e^G of rows of Q
+    float2 all = make_float2(0.0f, 0.0f);   // as chain_kernel's
     uint4 v[kCols / 8];
     auto fetch = [&](int c) {
       const int64_t tok = start + static_cast<int64_t>(c) * C + row;
       const float* g = reinterpret_cast<const float*>(
           a.tt + ((static_cast<int64_t>(slot0) + c) * a.h_v + h) * kHeadBytes + 2 * kTTBytes);
       gate = g[(is_v ? C : 0) + row];
-      eall = g[3 * C];
+      all = *reinterpret_cast<const float2*>(g + 3 * C);
 #pragma unroll
       for (int u = 0; u < kCols / 8; ++u) {
         v[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -1189,18 +1219,19 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
       const uint32_t par = c & 1, before = par ^ 1;
       float D[kCols], AV[kCols];
       if (c > 0) {
-        if (!(ok = warp_wait(d3, before, abort_flag, kFaultChain))) break;
+        if (!(ok = warp_wait(d3, before, abort_flag, kFaultChain, a.wait_limit_ns))) break;
         ptx::tc_fence_after();
         ld_sum<kPieces, DVB>(lanes + P::D3, D);
-        if (!(ok = warp_wait(d2, before, abort_flag, kFaultChain))) break;
+        if (!(ok = warp_wait(d2, before, abort_flag, kFaultChain, a.wait_limit_ns))) break;
         ptx::tc_fence_after();
         if (!is_v) {
           ptx::tc_ld_32x32b_x16(lanes + P::D2, AV);
           ptx::tc_wait_ld();
         }
       }
-      const float eg = gate, e_all = eall;
+      const float eg = gate, e_all = all.x;
       if (c < n) {
+        if (!(ok = prepared(all.y, abort_flag))) break;
         if (is_v) {
           float u[kCols];
 #pragma unroll
@@ -1223,7 +1254,7 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
       if (c > 0) {
 #pragma unroll
         for (int j = 0; j < kCols; ++j) S[j] = eall_before * S[j] + D[j];
-        if (!(ok = warp_wait(d1, before, abort_flag, kFaultChain))) break;
+        if (!(ok = warp_wait(d1, before, abort_flag, kFaultChain, a.wait_limit_ns))) break;
         ptx::tc_fence_after();
       }
       if (c > 0 && !is_v) ld_sum<kSPieces, DVB>(lanes + P::D1, D);  // Q S

@@ -1292,6 +1292,17 @@ nvfp4_status launch_linear_attention(DeviceState* st, const nvfp4::la::Args& a, 
                    PlainCfg<DK, 32, 2>::SMEM);
 }
 
+// nvfp4_linear_attention; the stalls and the limit only for its self-test.
+nvfp4_status linear_attention_entry(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                    const void* v, int64_t ldv, const float* decay,
+                                    const float* beta, float scale, int64_t total, int h_k,
+                                    int h_v, int d_k, int d_v, int64_t n_seq,
+                                    const int32_t* cu_seqlens, float* state, int64_t n_slots,
+                                    const int32_t* slots, const int32_t* resume, void* o,
+                                    int64_t ldo, void* workspace, size_t workspace_bytes,
+                                    nvfp4_stream_t stream, int stall_prepare, int stall_chain,
+                                    uint64_t limit_ns);
+
 }  // namespace
 
 extern "C" {
@@ -1312,6 +1323,39 @@ nvfp4_status nvfp4_linear_attention(const void* q, int64_t ldq, const void* k, i
                                     const int32_t* slots, const int32_t* resume, void* o,
                                     int64_t ldo, void* workspace, size_t workspace_bytes,
                                     nvfp4_stream_t stream) {
+  return linear_attention_entry(q, ldq, k, ldk, v, ldv, decay, beta, scale, total, h_k, h_v, d_k,
+                                d_v, n_seq, cu_seqlens, state, n_slots, slots, resume, o, ldo,
+                                workspace, workspace_bytes, stream, -1, -1,
+                                nvfp4::la::kWaitLimitNs);
+}
+
+nvfp4_status nvfp4_selftest_linear_attention_stall(
+    const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+    const float* decay, const float* beta, float scale, int64_t total, int h_k, int h_v, int d_k,
+    int d_v, int64_t n_seq, const int32_t* cu_seqlens, float* state, int64_t n_slots,
+    const int32_t* slots, const int32_t* resume, void* o, int64_t ldo, void* workspace,
+    size_t workspace_bytes, int kernel, int cta, uint64_t limit_ns, nvfp4_stream_t stream) {
+  if (limit_ns < 1000u || limit_ns > 10000000000ull || kernel < 0 || kernel > 1 || cta < 0)
+    return NVFP4_ERR_INVALID_ARG;
+  return linear_attention_entry(q, ldq, k, ldk, v, ldv, decay, beta, scale, total, h_k, h_v, d_k,
+                                d_v, n_seq, cu_seqlens, state, n_slots, slots, resume, o, ldo,
+                                workspace, workspace_bytes, stream, kernel == 0 ? cta : -1,
+                                kernel == 1 ? cta : -1, limit_ns);
+}
+
+}  // extern "C"
+
+namespace {
+
+nvfp4_status linear_attention_entry(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                    const void* v, int64_t ldv, const float* decay,
+                                    const float* beta, float scale, int64_t total, int h_k,
+                                    int h_v, int d_k, int d_v, int64_t n_seq,
+                                    const int32_t* cu_seqlens, float* state, int64_t n_slots,
+                                    const int32_t* slots, const int32_t* resume, void* o,
+                                    int64_t ldo, void* workspace, size_t workspace_bytes,
+                                    nvfp4_stream_t stream, int stall_prepare, int stall_chain,
+                                    uint64_t limit_ns) {
   using namespace nvfp4::la;
   if (nvfp4_status e = check_heads(q, ldq, k, ldk, v, ldv, decay, beta, total, h_k, h_v, d_k, d_v,
                                    state, n_slots, slots, o, ldo))
@@ -1354,9 +1398,16 @@ nvfp4_status nvfp4_linear_attention(const void* q, int64_t ldq, const void* k, i
   a.o = static_cast<__nv_bfloat16*>(o);
   a.kq = static_cast<uint8_t*>(workspace);
   a.tt = a.kq + chunk_slots(total, n_seq) * h_k * kq_bytes(d_k);
+  a.wait_limit_ns = limit_ns;
+  a.stall_prepare = stall_prepare;
+  a.stall_chain = stall_chain;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return d_k == 128 ? launch_linear_attention<128>(st, a, s) : launch_linear_attention<64>(st, a, s);
 }
+
+}  // namespace
+
+extern "C" {
 
 nvfp4_status nvfp4_linear_attention_step(const void* q, int64_t ldq, const void* k, int64_t ldk,
                                          const void* v, int64_t ldv, const float* decay,

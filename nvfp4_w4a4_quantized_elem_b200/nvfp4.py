@@ -39,7 +39,8 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_sf_bytes", "nvfp4_quantize_workspace_by
            "nvfp4_fuse_group_scales", "nvfp4_silu_mul", "nvfp4_read_fault",
            "nvfp4_linear_attention_workspace_bytes", "nvfp4_linear_attention",
            "nvfp4_linear_attention_step",
-           "nvfp4_selftest_wait_timeout", "nvfp4_selftest_gemm_stall")
+           "nvfp4_selftest_wait_timeout", "nvfp4_selftest_gemm_stall",
+           "nvfp4_selftest_linear_attention_stall")
 
 _BF16, _FP32 = torch.bfloat16, torch.float32
 
@@ -69,6 +70,8 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, I64, I, SZ, U32P = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                ctypes.c_size_t, ctypes.POINTER(ctypes.c_uint32))
+        prompts = [P, I64, P, I64, P, I64, P, P, ctypes.c_float, I64, I, I, I, I, I64, P, P, I64,
+                   P, P, P, I64, P, SZ]
         sigs = {
             "nvfp4_status_string": (ctypes.c_char_p, [I]),
             "nvfp4_sf_bytes": (SZ, [I64, I64]),
@@ -91,8 +94,8 @@ def lib() -> ctypes.CDLL:
             "nvfp4_fuse_group_scales": (I, [I, P, I64, P, P, P, P, P]),
             "nvfp4_silu_mul": (I, [P, I64, I64, I64, P, I64, P]),
             "nvfp4_linear_attention_workspace_bytes": (SZ, [I64, I64, I, I, I]),
-            "nvfp4_linear_attention": (I, [P, I64, P, I64, P, I64, P, P, ctypes.c_float, I64, I, I,
-                                           I, I, I64, P, P, I64, P, P, P, I64, P, SZ, P]),
+            "nvfp4_linear_attention": (I, [*prompts, P]),
+            "nvfp4_selftest_linear_attention_stall": (I, [*prompts, I, I, ctypes.c_uint64, P]),
             "nvfp4_linear_attention_step": (I, [P, I64, P, I64, P, I64, P, P, ctypes.c_float, I64,
                                                 I, I, I, I, P, I64, P, P, I64, P]),
             "nvfp4_read_fault": (I, [P, U32P]),
@@ -534,6 +537,13 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
     [n_seq], None: in order), and come from there where ``resume`` (int32
     [n_seq]) is nonzero. ``scale`` defaults to d_k ** -0.5. The workspace is
     allocated here when None."""
+    return _prompts("nvfp4_linear_attention", (), q, k, v, decay, beta, cu_seqlens, state, slots,
+                    resume, scale, out, workspace, stream)
+
+
+def _prompts(call, more, q, k, v, decay, beta, cu_seqlens, state, slots, resume, scale, out,
+             workspace, stream):
+    """linear_attention, or its self-test: ``more`` are its further arguments."""
     hk, hv, dk, dv, (ldq, ldk, ldv, ldo), out = _heads(q, k, v, decay, beta, state, out, stream)
     total = q.shape[0]
     n_seq = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
@@ -543,12 +553,12 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
     if workspace is None:
         need = linear_attention_workspace_bytes(total, n_seq, hk, hv, dk)
         workspace = _empty(need, torch.uint8, q.device, stream)
-    st = lib().nvfp4_linear_attention(
+    st = getattr(lib(), call)(
         _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(decay), _ptr(beta),
         dk ** -0.5 if scale is None else scale, total, hk, hv, dk, dv, n_seq, _ptr(cu_seqlens),
         _ptr(state), 0 if state is None else state.shape[0], _ptr(slots), _ptr(resume), _ptr(out),
-        ldo, *_scratch(workspace, q.get_device()), _stream(stream))
-    _check(st, "nvfp4_linear_attention")
+        ldo, *_scratch(workspace, q.get_device()), *more, _stream(stream))
+    _check(st, call)
     return out
 
 
@@ -602,6 +612,23 @@ def selftest_gemm_stall(a: NVFP4Tensor, b: NVFP4Tensor, limit_ns: int = 1_000_00
                                            _ptr(y), m, n, k, limit_ns, *_scratch(workspace, dev),
                                            _stream(stream)),
            "nvfp4_selftest_gemm_stall")
+
+
+def selftest_linear_attention_stall(
+        q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
+        beta: torch.Tensor | None = None, *, kernel: int, cta: int = 0, limit_ns: int = 1_000_000,
+        cu_seqlens: torch.Tensor | None = None, state: torch.Tensor | None = None,
+        slots: torch.Tensor | None = None, resume: torch.Tensor | None = None,
+        scale: float | None = None, out: torch.Tensor | None = None,
+        workspace: torch.Tensor | None = None,
+        stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """nvfp4_selftest_linear_attention_stall: linear_attention with CTA ``cta`` of
+    its first (``kernel`` 0) or second (1) kernel never issuing its first product
+    or load, and every wait limited to ``limit_ns``: it gives up and returns, its
+    head's state stays as it was (read_fault() then returns 512, or 1024 and / or
+    2048)."""
+    return _prompts("nvfp4_selftest_linear_attention_stall", (kernel, cta, limit_ns), q, k, v,
+                    decay, beta, cu_seqlens, state, slots, resume, scale, out, workspace, stream)
 
 
 def linear_workspace_bytes(m: int, n: int, k: int) -> int:

@@ -485,6 +485,7 @@ size_t nvfp4_linear_attention_workspace_bytes(int64_t total, int64_t n_seq, int 
  *              nvfp4_linear_attention_workspace_bytes(...) bytes, owned by the
  *              caller, not shared with a call that may run at the same time; no
  *              initialisation needed.
+ *   Neither the workspace nor the pool of states may overlap any other argument.
  *   h_v % h_k == 0; d_k 64 or 128; d_v % 32 == 0; all row pitches multiples of
  *   8 elements; q, k, v, o, state 16-byte aligned.
  * Two kernels. MMA operands made from FP32 values are cut into bf16 pieces:

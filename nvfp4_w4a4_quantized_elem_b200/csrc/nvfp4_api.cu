@@ -774,6 +774,14 @@ nvfp4_status gemm_paired(PFN_cuTensorMapEncodeTiled_v12000 enc, DeviceState* st,
                     stream, 2u, tmA, tmB, tmSFA, tmSFB, tmY, p);
 }
 
+// Bytes from the first to the last element of [rows][cols] at pitch ld; what no
+// address space holds counts as 2^62.
+int64_t span_bytes(int64_t rows, int64_t ld, int64_t cols, int64_t esize) {
+  if (rows < 1 || cols < 1) return 0;
+  const __int128 n = (static_cast<__int128>(rows - 1) * ld + cols) * esize;
+  return n < (int64_t{1} << 62) ? static_cast<int64_t>(n) : int64_t{1} << 62;
+}
+
 // Whether two [rows][..] matrices share bytes: `ca` columns of `ea` bytes at
 // pitch lda, `cb` of `eb` bytes at pitch ldb. Disjoint columns of one matrix
 // (same pitch in bytes) do not.
@@ -782,8 +790,8 @@ bool rows_overlap(const void* a, int64_t lda, int64_t ca, int64_t ea, const void
   if (a == nullptr || b == nullptr || rows < 1) return false;
   const int64_t a0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a));
   const int64_t b0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b));
-  const int64_t a1 = a0 + ((rows - 1) * lda + ca) * ea, b1 = b0 + ((rows - 1) * ldb + cb) * eb;
-  if (a1 <= b0 || b1 <= a0) return false;
+  if (a0 < b0 ? a0 + span_bytes(rows, lda, ca, ea) <= b0 : b0 + span_bytes(rows, ldb, cb, eb) <= a0)
+    return false;
   if (rows == 1 || lda * ea != ldb * eb) return true;
   const int64_t ld = lda * ea;
   const int64_t d = (((b0 - a0) % ld) + ld) % ld;  // b's column offset from a, in bytes
@@ -1202,14 +1210,33 @@ nvfp4_status nvfp4_fuse_group_scales(int n_modules, const int64_t* rows_per_modu
 namespace {
 
 bool bytes_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  return rows_overlap(a, na, na, 1, b, nb, nb, 1, 1);
+  return na > 0 && nb > 0 && rows_overlap(a, na, na, 1, b, nb, nb, 1, 1);
 }
 
-// What both linear-attention calls ask of their heads and rows.
+// Device memory of one argument, from its first to its last byte.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+
+// Whether what is written (`p`, null: nothing) meets one of the inputs.
+template <size_t N>
+bool overlaps_any(const Span& w, const Span (&inputs)[N]) {
+  for (const Span& i : inputs)
+    if (bytes_overlap(w.p, w.bytes, i.p, i.bytes)) return true;
+  return false;
+}
+
+int64_t pool_bytes(int64_t n_slots, int64_t wv, int64_t d_k) {
+  return span_bytes(n_slots, wv * d_k, wv * d_k, 4);
+}
+
+// What both linear-attention calls ask of their heads and rows; slots holds
+// n_slot_ids numbers.
 nvfp4_status check_heads(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
                          int64_t ldv, const float* decay, const float* beta, int64_t rows, int h_k,
                          int h_v, int d_k, int d_v, const float* state, int64_t n_slots,
-                         const int32_t* slots, const void* o, int64_t ldo) {
+                         const int32_t* slots, int64_t n_slot_ids, const void* o, int64_t ldo) {
   if (rows < 0 || h_k < 1 || h_v < 1 || d_k < 1 || d_v < 1 || n_slots < 0) return NVFP4_ERR_INVALID_ARG;
   if (rows > 0 && (!q || !k || !v || !decay || !o)) return NVFP4_ERR_INVALID_ARG;
   if (h_v % h_k != 0) return NVFP4_ERR_INVALID_ARG;
@@ -1226,9 +1253,13 @@ nvfp4_status check_heads(const void* q, int64_t ldq, const void* k, int64_t ldk,
       rows_overlap(o, ldo, wv, 2, k, ldk, wk, 2, rows) ||
       rows_overlap(o, ldo, wv, 2, v, ldv, wv, 2, rows))
     return NVFP4_ERR_INVALID_ARG;
-  const int64_t ob = rows > 0 ? ((rows - 1) * ldo + wv) * 2 : 0;
-  if (bytes_overlap(o, ob, decay, rows * h_v * 4) || bytes_overlap(o, ob, beta, rows * h_v * 4) ||
-      bytes_overlap(o, ob, state, n_slots * wv * d_k * 4))
+  // o (between whose rows there may be others of q, k or v) over anything else,
+  // and the pool over anything at all
+  const Span out{o, span_bytes(rows, ldo, wv, 2)}, pool{state, pool_bytes(n_slots, wv, d_k)};
+  const Span gates[] = {{decay, rows * h_v * 4}, {beta, rows * h_v * 4}, {slots, n_slot_ids * 4}};
+  const Span rows_in[] = {{q, span_bytes(rows, ldq, wk, 2)}, {k, span_bytes(rows, ldk, wk, 2)},
+                          {v, span_bytes(rows, ldv, wv, 2)}, out};
+  if (overlaps_any(out, gates) || overlaps_any(pool, gates) || overlaps_any(pool, rows_in))
     return NVFP4_ERR_INVALID_ARG;
   return NVFP4_OK;
 }
@@ -1358,7 +1389,7 @@ nvfp4_status linear_attention_entry(const void* q, int64_t ldq, const void* k, i
                                     uint64_t limit_ns) {
   using namespace nvfp4::la;
   if (nvfp4_status e = check_heads(q, ldq, k, ldk, v, ldv, decay, beta, total, h_k, h_v, d_k, d_v,
-                                   state, n_slots, slots, o, ldo))
+                                   state, n_slots, slots, n_seq, o, ldo))
     return e;
   if (n_seq < 1 || workspace == nullptr || (cu_seqlens == nullptr && n_seq != 1) ||
       (state == nullptr && (slots != nullptr || resume != nullptr)) ||
@@ -1368,7 +1399,18 @@ nvfp4_status linear_attention_entry(const void* q, int64_t ldq, const void* k, i
     return NVFP4_ERR_UNSUPPORTED;
   if (!aligned(workspace, 256) || !aligned(cu_seqlens, 4) || !aligned(resume, 4))
     return NVFP4_ERR_MISALIGNED;
-  if (workspace_bytes < nvfp4_linear_attention_workspace_bytes(total, n_seq, h_k, h_v, d_k))
+  const size_t need = nvfp4_linear_attention_workspace_bytes(total, n_seq, h_k, h_v, d_k);
+  if (workspace_bytes < need) return NVFP4_ERR_INVALID_ARG;
+  const int64_t wk = static_cast<int64_t>(h_k) * d_k, wv = static_cast<int64_t>(h_v) * d_v;
+  const Span scratch{workspace, static_cast<int64_t>(need)};
+  const Span out{o, span_bytes(total, ldo, wv, 2)}, pool{state, pool_bytes(n_slots, wv, d_k)};
+  const Span offsets[] = {{cu_seqlens, cu_seqlens != nullptr ? (n_seq + 1) * 4 : 0},
+                          {resume, n_seq * 4}};
+  const Span others[] = {{q, span_bytes(total, ldq, wk, 2)}, {k, span_bytes(total, ldk, wk, 2)},
+                         {v, span_bytes(total, ldv, wv, 2)}, {decay, total * h_v * 4},
+                         {beta, total * h_v * 4}, {slots, n_seq * 4}, out, pool};
+  if (overlaps_any(scratch, others) || overlaps_any(scratch, offsets) ||
+      overlaps_any(out, offsets) || overlaps_any(pool, offsets))
     return NVFP4_ERR_INVALID_ARG;
   int dev;
   DeviceState* st;
@@ -1417,7 +1459,7 @@ nvfp4_status nvfp4_linear_attention_step(const void* q, int64_t ldq, const void*
                                          nvfp4_stream_t stream) {
   using namespace nvfp4::la;
   if (nvfp4_status e = check_heads(q, ldq, k, ldk, v, ldv, decay, beta, batch, h_k, h_v, d_k, d_v,
-                                   state, n_slots, slots, o, ldo))
+                                   state, n_slots, slots, batch, o, ldo))
     return e;
   if (state == nullptr || (slots == nullptr && n_slots < batch)) return NVFP4_ERR_INVALID_ARG;
   const int cols = step_cols(d_k, d_v);

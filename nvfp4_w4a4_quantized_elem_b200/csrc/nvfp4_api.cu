@@ -1253,15 +1253,24 @@ nvfp4_status check_heads(const void* q, int64_t ldq, const void* k, int64_t ldk,
       rows_overlap(o, ldo, wv, 2, k, ldk, wk, 2, rows) ||
       rows_overlap(o, ldo, wv, 2, v, ldv, wv, 2, rows))
     return NVFP4_ERR_INVALID_ARG;
-  // o (between whose rows there may be others of q, k or v) over anything else,
-  // and the pool over anything at all
-  const Span out{o, span_bytes(rows, ldo, wv, 2)}, pool{state, pool_bytes(n_slots, wv, d_k)};
-  const Span gates[] = {{decay, rows * h_v * 4}, {beta, rows * h_v * 4}, {slots, n_slot_ids * 4}};
-  const Span rows_in[] = {{q, span_bytes(rows, ldq, wk, 2)}, {k, span_bytes(rows, ldk, wk, 2)},
-                          {v, span_bytes(rows, ldv, wv, 2)}, out};
-  if (overlaps_any(out, gates) || overlaps_any(pool, gates) || overlaps_any(pool, rows_in))
-    return NVFP4_ERR_INVALID_ARG;
-  return NVFP4_OK;
+  const Span out{o, span_bytes(rows, ldo, wv, 2)};
+  const Span others[] = {{decay, rows * h_v * 4}, {beta, rows * h_v * 4}, {slots, n_slot_ids * 4},
+                         {state, pool_bytes(n_slots, wv, d_k)}};
+  return overlaps_any(out, others) ? NVFP4_ERR_INVALID_ARG : NVFP4_OK;
+}
+
+// The pool of states over an input (o: check_heads). Asked last, when the sizes
+// are known to be supported.
+nvfp4_status check_pool(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                        int64_t ldv, const float* decay, const float* beta, int64_t rows, int h_k,
+                        int h_v, int d_k, int d_v, const float* state, int64_t n_slots,
+                        const int32_t* slots, int64_t n_slot_ids) {
+  const int64_t wk = static_cast<int64_t>(h_k) * d_k, wv = static_cast<int64_t>(h_v) * d_v;
+  const Span pool{state, pool_bytes(n_slots, wv, d_k)};
+  const Span inputs[] = {{q, span_bytes(rows, ldq, wk, 2)}, {k, span_bytes(rows, ldk, wk, 2)},
+                         {v, span_bytes(rows, ldv, wv, 2)}, {decay, rows * h_v * 4},
+                         {beta, rows * h_v * 4}, {slots, n_slot_ids * 4}};
+  return overlaps_any(pool, inputs) ? NVFP4_ERR_INVALID_ARG : NVFP4_OK;
 }
 
 // Chunk slots of the workspace: first_slot() of linear_attention.cuh.
@@ -1399,6 +1408,9 @@ nvfp4_status linear_attention_entry(const void* q, int64_t ldq, const void* k, i
     return NVFP4_ERR_UNSUPPORTED;
   if (!aligned(workspace, 256) || !aligned(cu_seqlens, 4) || !aligned(resume, 4))
     return NVFP4_ERR_MISALIGNED;
+  if (nvfp4_status e = check_pool(q, ldq, k, ldk, v, ldv, decay, beta, total, h_k, h_v, d_k, d_v,
+                                  state, n_slots, slots, n_seq))
+    return e;
   const size_t need = nvfp4_linear_attention_workspace_bytes(total, n_seq, h_k, h_v, d_k);
   if (workspace_bytes < need) return NVFP4_ERR_INVALID_ARG;
   const int64_t wk = static_cast<int64_t>(h_k) * d_k, wv = static_cast<int64_t>(h_v) * d_v;
@@ -1465,6 +1477,9 @@ nvfp4_status nvfp4_linear_attention_step(const void* q, int64_t ldq, const void*
   const int cols = step_cols(d_k, d_v);
   const int64_t grid = batch * h_v * (d_v / cols);
   if (grid >= (int64_t{1} << 31)) return NVFP4_ERR_UNSUPPORTED;
+  if (nvfp4_status e = check_pool(q, ldq, k, ldk, v, ldv, decay, beta, batch, h_k, h_v, d_k, d_v,
+                                  state, n_slots, slots, batch))
+    return e;
   if (batch == 0) return NVFP4_OK;
   StepArgs a;
   std::memset(&a, 0, sizeof a);

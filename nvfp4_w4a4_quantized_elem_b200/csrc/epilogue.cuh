@@ -6,7 +6,7 @@
 // product; the epilogue is the model's own and is written from the formulas:
 //   relu       max(z, 0)
 //   silu       z / (1 + e^-z)
-//   gelu       z/2 (1 + erf(z / sqrt 2))
+//   gelu       z/2 (1 + erf(z / sqrt 2)) = z Phi(z)
 //   gelu_tanh  z/2 (1 + tanh u) = z / (1 + e^-2u), u = sqrt(2/pi) (z + 0.044715 z^3)
 // Without the fusion the bf16 product makes one more round trip through
 // memory per step (2 m n bytes written, read and written again) and is
@@ -37,14 +37,31 @@ __device__ __forceinline__ float over_one_plus_ex2(float z, float t) {
   return z * ptx::rcp(1.0f + ptx::ex2(t));
 }
 
+// z Phi(z) = max(z, 0) - |z| Q(|z|), Q(a) = erfc(a / sqrt 2) / 2, without the
+// cancellation of z/2 + z/2 erf, which leaves no digit below z = -5.5. Q(a) =
+// e^{-a^2/2} F(a) with F smooth: t P(t) with t = 1 / (1 + 0.3 a), P of degree 7
+// fitted to the least largest relative error on [0, 14.5] (1.7e-7, a linear
+// program). What is left is the exponential's, |z|^2/2 steps in the far tail.
+// Beyond |z| = 20, where Q is below 1e-88, |z| stands at 20 (so that -inf gives 0).
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fminf(fabsf(z), 20.0f);
+  const float t = ptx::rcp(fmaf(0.3f, a, 1.0f));
+  float p = fmaf(0.0354235582f, t, -0.156157714f);
+  p = fmaf(p, t, 0.204555524f);
+  p = fmaf(p, t, -0.0520328607f);
+  p = fmaf(p, t, 0.127691165f);
+  p = fmaf(p, t, 0.100176129f);
+  p = fmaf(p, t, 0.120712108f);
+  p = fmaf(p, t, 0.119632009f);
+  const float q = (p * t) * ptx::ex2((a * a) * -0.72134752f);  // 2^(-a^2/2 log2(e))
+  return fmaf(-a, q, z < 0.0f ? 0.0f : z);  // (a NaN stays one)
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if (ACT == kRelu) return z < 0.0f ? 0.0f : z;  // (a NaN stays one)
   if (ACT == kSilu) return over_one_plus_ex2(z, -1.44269504f * z);
-  if (ACT == kGelu) {  // erff: 2 ulp; erfcf would keep the far tail's digits at 4x the time
-    const float h = 0.5f * z;
-    return fmaf(h, erff(0.70710678f * z), h);
-  }
+  if (ACT == kGelu) return gelu(z);
   if (ACT == kGeluTanh)  // -2u log2(e) = z (-2.30220819 - 0.102943240 z^2)
     return over_one_plus_ex2(z, z * fmaf(z * z, -0.102943240f, -2.30220819f));
   return z;

@@ -495,8 +495,10 @@ size_t nvfp4_linear_attention_workspace_bytes(int64_t total, int64_t n_seq, int 
  * rounding to bf16.
  * Results do not depend on the run or on the other sequences of the call.
  * A NaN or an infinity in a token's inputs reaches the later tokens of its
- * sequence, as in the formula, and also the earlier ones of its 64-token chunk
- * (their zero factors multiply it); other sequences and heads stay clean.
+ * sequence, as in the formula, and no earlier one, other sequence or head. (Where
+ * an output is not finite, the sequence's tokens are gone over once more, one by
+ * one, by the CTAs of that head and of those columns of d_v: the outputs from that
+ * 64-token chunk on and the state come from there, about 2 us a token.)
  * A wait that runs out (nvfp4_read_fault: bit 512 the first kernel, 1024 and
  * 2048 the second) ends its head of its sequence: the state stays as it was, in
  * the second kernel that of the CTA's columns of d_v, and the rows of o are left

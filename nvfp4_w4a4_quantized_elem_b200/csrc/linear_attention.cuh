@@ -38,9 +38,17 @@
 // alone would leave 2^-9 in the states. G is summed in FP64 and kept as two
 // FP32 parts: the difference of two FP32 sums of strong decays would lose the
 // weak decays between them.
+//
+// What is not finite. A chunk's products reach every row of it, with zeros where
+// the recurrence has nothing, and zero times a NaN is one: an infinity or a NaN in a
+// token also reaches the tokens before it in its chunk. The chains look at the
+// outputs as they store them and, where one is not finite, go over the
+// sequence again when they are through, token by token, with its outputs from that
+// chunk on and its state from there.
 #pragma once
 
 #include <cuda_bf16.h>
+#include <climits>
 #include <cstdint>
 
 #include "fault.cuh"
@@ -502,7 +510,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       const double y = __shfl_up_sync(0xFFFFFFFFu, s, d);
       if (lane >= d) s += y;
     }
-    const double s0 = s - x1;
+    // (a token's decay does not reach the one before it)
+    const double before = __shfl_up_sync(0xFFFFFFFFu, s, 1);
+    const double s0 = fabs(x1) < INFINITY ? s - x1 : (lane > 0 ? before : 0.0) + x0;
     const float h0 = static_cast<float>(s0), h1 = static_cast<float>(s);
     G[2 * lane] = make_float2(h0, static_cast<float>(s0 - h0));
     G[2 * lane + 1] = make_float2(h1, static_cast<float>(s - h1));
@@ -735,9 +745,97 @@ __device__ __forceinline__ bool prepared(float word, volatile uint32_t* abort_fl
   return false;
 }
 
-// o = scale (e^G (Q S) + A U), 16 columns of one token.
-__device__ __forceinline__ void store_out(__nv_bfloat16* o, float scale, float eg,
+struct StateRow {
+  float x[kCols];
+};
+
+// The tokens [tok, end) one by one, by the four warps that hold the rows of 16
+// columns of S: as step_kernel does, with the sums over d_k by shuffles and, between
+// the warps, through `scratch`, two tokens' worth in turns (one barrier a token).
+// Outputs from token `from` on.
+static_assert(2 * kCols == 32, "a sum per lane");
+constexpr int kTokenFloats = 2 * kCols + 1;            // S^T k, S^T q, q.k of a warp's rows
+constexpr int kScratchBytes = 2 * 4 * kTokenFloats * 4;   // per 16 columns
+
+template <int DK>
+__device__ __noinline__ StateRow token_by_token(const Args& a, float* scratch, int64_t tok, int64_t end,
+                                                int64_t from, int h, int64_t col, int warp, int lane,
+                                                StateRow S) {
+  const int k_row = (warp & 3) * 32 + lane, hk = h / (a.h_v / a.h_k);
+  const bool live = k_row < DK;
+  const int64_t at = static_cast<int64_t>(hk) * DK + k_row;
+  // a token's inputs, asked for a token ahead
+  __nv_bfloat16 k = {}, q = {};
+  float g = 0.0f, beta = 0.0f;
+  uint4 v[kCols / 8];
+  const auto fetch = [&](int64_t t) {
+    if (live) {
+      k = a.k[t * a.ldk + at];
+      q = a.q[t * a.ldq + at];
+    }
+    g = a.decay[t * a.h_v + h];
+    if (a.beta != nullptr) beta = a.beta[t * a.h_v + h];
+#pragma unroll
+    for (int u = 0; u < kCols / 8; ++u)
+      v[u] = *reinterpret_cast<const uint4*>(a.v + t * a.ldv + col + 8 * u);
+  };
+  if (tok < end) fetch(tok);
+#pragma unroll 1
+  for (int turn = 0; tok < end; ++tok, turn ^= 1) {
+    const float kk = __bfloat162float(k), qq = __bfloat162float(q), e = expf(g), b = beta;
+    uint4 vv[kCols / 8];
+#pragma unroll
+    for (int u = 0; u < kCols / 8; ++u) vv[u] = v[u];
+    if (tok + 1 < end) fetch(tok + 1);
+    // 32 sums over the lanes, halved as they go: lane i is left with sum i
+    float x[2 * kCols], qk = live ? kk * qq : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      x[j] = live ? kk * S.x[j] : 0.0f;
+      x[kCols + j] = live ? qq * S.x[j] : 0.0f;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+#pragma unroll
+      for (int j = 0; j < d; ++j) {
+        const bool up = (lane & d) != 0;
+        const float give = up ? x[j] : x[j + d], keep = up ? x[j + d] : x[j];
+        x[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, d);
+      }
+      qk += __shfl_xor_sync(0xFFFFFFFFu, qk, d);
+    }
+    float* const all = scratch + turn * 4 * kTokenFloats;
+    float* const mine = all + (warp & 3) * kTokenFloats;
+    mine[lane] = x[0];
+    if (lane == 0) mine[2 * kCols] = qk;
+    if (warp < 4)  // the warps of these columns
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    else
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+    const auto sum = [&](int j) {
+      return (all[j] + all[kTokenFloats + j]) + (all[2 * kTokenFloats + j] + all[3 * kTokenFloats + j]);
+    };
+    qk = sum(2 * kCols);
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const uint4& w = vv[j / 8];
+      const uint32_t pair = j % 8 < 2 ? w.x : j % 8 < 4 ? w.y : j % 8 < 6 ? w.z : w.w;
+      const float vj = __uint_as_float((j & 1) != 0 ? pair & 0xFFFF0000u : pair << 16);
+      const float u = a.beta != nullptr ? b * (vj - e * sum(j)) : vj;
+      if (k_row == 0 && tok >= from)
+        a.o[tok * a.ldo + col + j] = __float2bfloat16_rn(a.scale * (e * sum(kCols + j) + qk * u));
+      S.x[j] = live ? e * S.x[j] + kk * u : 0.0f;
+    }
+  }
+  return S;
+}
+
+// o = scale (e^G (Q S) + A U), 16 columns of one token. Whether one of them is not
+// finite: 0 x is 0 or NaN.
+__device__ __forceinline__ bool store_out(__nv_bfloat16* o, float scale, float eg,
                                           const float (&qs)[kCols], const float (&au)[kCols]) {
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+  __nv_bfloat162 z = zero;
 #pragma unroll
   for (int u = 0; u < kCols / 8; ++u) {
     uint32_t w[4];
@@ -745,9 +843,11 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* o, float scale, float e
     for (int e = 0; e < 4; ++e) {
       const int j = 8 * u + 2 * e;
       w[e] = round_piece(scale * (eg * qs[j] + au[j]), scale * (eg * qs[j + 1] + au[j + 1]));
+      z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zero, z);
     }
     *reinterpret_cast<uint4*>(o + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  return (*reinterpret_cast<const uint32_t*>(&z) & 0x7FFF7FFFu) != 0u;
 }
 
 // This thread's 16 columns of the BLOCKS column blocks of a result, added.
@@ -766,7 +866,7 @@ __device__ __forceinline__ void ld_sum(uint32_t taddr, float (&x)[kCols]) {
 
 template <int DK, int DVB>
 __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
-    chain_kernel(const Args a) {
+    chain_kernel(const __grid_constant__ Args a) {
   using P = ChainCfg<DK, DVB>;
   extern __shared__ __align__(1024) uint8_t smem_la[];
   uint8_t* const smem = smem_la;
@@ -781,6 +881,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
   uint64_t* const drain = full + 9;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(full + 10);
   volatile uint32_t* const abort_flag = tmem_holder + 1;
+  int* const not_finite = reinterpret_cast<int*>(tmem_holder + 2);  // first such chunk
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int blocks = a.d_v / DVB;
@@ -800,6 +901,7 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
     ptx::mbar_init(d3, 1);
     ptx::mbar_init(full_tt, 1);
     ptx::mbar_init(drain, 1);
+    *not_finite = INT_MAX;
     // the swizzled images need the alignment that the declaration asks for
     *abort_flag = (ptx::smem_u32(smem) & 1023u) != 0u ? 1u : 0u;
     if (*abort_flag) atomicOr(&g_fault_word, kFaultChain);
@@ -978,13 +1080,25 @@ __global__ void __launch_bounds__(ChainCfg<DK, DVB>::THREADS, 2)
         store_row_split<kPieces>(r_x, P::X_PIECE, row, C * 16, D);
         publish(u_ready);
       } else if (tok < end) {
-        store_out(a.o + tok * a.ldo + col, a.scale, eg_c, Q, D);
+        if (store_out(a.o + tok * a.ldo + col, a.scale, eg_c, Q, D)) atomicMin(not_finite, c);
       }
       if (!(ok = warp_wait(d3, par, abort_flag, kFaultChain, a.wait_limit_ns))) break;
       ptx::tc_fence_after();
       ld_sum<kPieces, DVB>(lanes, D);
 #pragma unroll
       for (int j = 0; j < kCols; ++j) S[j] = eall_c * S[j] + D[j];
+    }
+    // every compute warp is through its chunks, and all products are complete
+    asm volatile("bar.sync 3, %0;" ::"n"(32 * P::WARPS) : "memory");
+    const int bad = *static_cast<volatile int*>(not_finite);
+    if (ok && *abort_flag == 0u && bad < n) {
+      StateRow row_of_s;
+      load_state(a, slot >= 0 && k_row < DK, b, state, row_of_s.x);
+      row_of_s = token_by_token<DK>(a, reinterpret_cast<float*>(smem + P::R_OFF + (warp >> 2) * kScratchBytes),
+                                    start, end, start + static_cast<int64_t>(bad) * C, h, col, warp, lane,
+                                    row_of_s);
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) S[j] = row_of_s.x[j];
     }
     if (ok && slot >= 0 && k_row < DK) store_state(state, S);
   }
@@ -1035,7 +1149,7 @@ struct PlainCfg {
 template <int DK, int DVB, int A_BUFS>
 __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
                                   PlainCfg<DK, DVB, A_BUFS>::PER_SM)
-    plain_kernel(const Args a) {
+    plain_kernel(const __grid_constant__ Args a) {
   using P = PlainCfg<DK, DVB, A_BUFS>;
   extern __shared__ __align__(1024) uint8_t smem_la[];
   uint8_t* const smem = smem_la;
@@ -1049,6 +1163,7 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
   uint64_t* const drain = full + 9;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(full + 10);
   volatile uint32_t* const abort_flag = tmem_holder + 1;
+  int* const not_finite = reinterpret_cast<int*>(tmem_holder + 2);  // first such chunk
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int blocks = a.d_v / DVB;
@@ -1067,6 +1182,7 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
     ptx::mbar_init(d2, 1);
     ptx::mbar_init(d3, 1);
     ptx::mbar_init(drain, 1);
+    *not_finite = INT_MAX;
     // the swizzled images need the alignment that the declaration asks for
     *abort_flag = (ptx::smem_u32(smem) & 1023u) != 0u ? 1u : 0u;
     if (*abort_flag) atomicOr(&g_fault_word, kFaultChain);
@@ -1264,10 +1380,23 @@ __global__ void __launch_bounds__(PlainCfg<DK, DVB, A_BUFS>::THREADS,
       }
       if (c > 0 && !is_v) {
         const int64_t tok = start + static_cast<int64_t>(c - 1) * C + row;
-        if (tok < end) store_out(a.o + tok * a.ldo + col, a.scale, eg_before, D, AV);
+        if (tok < end && store_out(a.o + tok * a.ldo + col, a.scale, eg_before, D, AV))
+          atomicMin(not_finite, c - 1);
       }
       eg_before = eg;
       eall_before = e_all;
+    }
+    // every compute warp is through its chunks, and all products are complete
+    asm volatile("bar.sync 3, %0;" ::"n"(32 * P::WARPS) : "memory");
+    const int bad = *static_cast<volatile int*>(not_finite);
+    if (ok && *abort_flag == 0u && bad < n) {
+      StateRow row_of_s;
+      load_state(a, slot >= 0 && k_row < DK, b, state, row_of_s.x);
+      row_of_s = token_by_token<DK>(a, reinterpret_cast<float*>(smem + P::V_OFF + (warp >> 2) * kScratchBytes),
+                                    start, end, start + static_cast<int64_t>(bad) * C, h, col, warp, lane,
+                                    row_of_s);
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) S[j] = row_of_s.x[j];
     }
     if (ok && slot >= 0 && k_row < DK) store_state(state, S);
   }

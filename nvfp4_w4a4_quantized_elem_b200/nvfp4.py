@@ -153,7 +153,11 @@ def _given(t: torch.Tensor, stream: torch.cuda.Stream | None) -> torch.Tensor:
     return t
 
 
-def _given_nvfp4(t: NVFP4Tensor, stream: torch.cuda.Stream | None) -> NVFP4Tensor:
+def _empty_nvfp4(rows: int, k: int, device, stream: torch.cuda.Stream | None) -> NVFP4Tensor:
+    if stream is None:
+        return NVFP4Tensor.empty(rows, k, device)
+    with torch.cuda.stream(stream):
+        t = NVFP4Tensor.empty(rows, k, device)
     for part in (t.codes, t.sf, t.global_scale):
         _given(part, stream)
     return t
@@ -186,9 +190,17 @@ def _global(g: torch.Tensor | None, name: str, dev: int) -> int | None:
 
 def _operand(t: NVFP4Tensor, name: str, dev: int) -> tuple[int, int, int]:
     """Pointers of codes, scales and global of an operand on cuda:``dev``."""
-    if dev < 0 or t.codes.get_device() != dev or t.sf.get_device() != dev:
+    codes, sf, g = t.codes, t.sf, t.global_scale
+    if dev < 0 or codes.get_device() != dev or sf.get_device() != dev or g.get_device() != dev:
         raise ValueError(f"{name} must be on the CUDA device of the call's other tensors")
-    return t.codes.data_ptr(), t.sf.data_ptr(), _global(t.global_scale, f"{name}'s global", dev)
+    return codes.data_ptr(), sf.data_ptr(), g.data_ptr()
+
+
+def _output(t: NVFP4Tensor, rows: int, k: int, dev: int) -> tuple[int, int, int]:
+    """The same of an output for [rows, k]."""
+    if (t.rows, t.k) != (rows, k):
+        raise ValueError(f"out must be an NVFP4 tensor for [{rows}, {k}]")
+    return _operand(t, "out", dev)
 
 
 def sf_bytes(rows: int, k: int) -> int:
@@ -209,11 +221,26 @@ class NVFP4Tensor:
     rows: int
     k: int
 
+    def __post_init__(self):
+        # once, not in every call: 8 bits each, codes [rows, k/2], scales padded to
+        # 128 rows and 4 blocks of 16; the calls hand them on as pointers
+        codes, sf, g = self.codes, self.sf, self.global_scale
+        if (codes.numel() * 2 < self.rows * self.k or codes.element_size() != 1
+                or sf.numel() < -(-self.rows // 128) * 128 * (-(-self.k // 64) * 4)
+                or sf.element_size() != 1 or not codes.is_contiguous() or not sf.is_contiguous()):
+            raise ValueError("an NVFP4 tensor needs contiguous 8-bit codes and scales for "
+                             f"[{self.rows}, {self.k}]")
+        if g.dtype is not _FP32 or g.numel() < 1:
+            raise ValueError(f"an NVFP4 tensor's global scale must be a {_FP32} element")
+
     @staticmethod
     def empty(rows: int, k: int, device="cuda") -> "NVFP4Tensor":
-        return NVFP4Tensor(torch.empty((rows, k // 2), dtype=torch.uint8, device=device),
-                           torch.empty(sf_bytes(rows, k), dtype=torch.uint8, device=device),
-                           torch.empty(1, dtype=torch.float32, device=device), rows, k)
+        t = object.__new__(NVFP4Tensor)  # right as made: without __post_init__
+        t.codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=device)
+        t.sf = torch.empty(sf_bytes(rows, k), dtype=torch.uint8, device=device)
+        t.global_scale = torch.empty(1, dtype=torch.float32, device=device)
+        t.rows, t.k = rows, k
+        return t
 
 
 def quantize(x: torch.Tensor, global_scale: torch.Tensor | None = None,
@@ -227,15 +254,13 @@ def quantize(x: torch.Tensor, global_scale: torch.Tensor | None = None,
         raise ValueError("x must be 2-D with unit stride along k")
     rows, k = x.shape
     if out is None:
-        with _on(stream):
-            out = NVFP4Tensor.empty(rows, k, x.device)
-        _given_nvfp4(out, stream)
+        out = _empty_nvfp4(rows, k, x.device, stream)
     if global_scale is None and workspace is None:
         workspace = _empty(quantize_workspace_bytes(rows, k), torch.uint8, x.device, stream)
     dev = x.get_device()
     st = lib().nvfp4_quantize(_ptr(x), rows, k, x.stride(0),
                               _global(global_scale, "global_scale", dev),
-                              *_operand(out, "out", dev), *_scratch(workspace, dev),
+                              *_output(out, rows, k, dev), *_scratch(workspace, dev),
                               _stream(stream))
     _check(st, "nvfp4_quantize")
     return out
@@ -254,7 +279,7 @@ def quantize_noalloc(x: torch.Tensor, out: NVFP4Tensor, global_scale: torch.Tens
     dev = x.get_device()
     st = lib().nvfp4_quantize_noalloc(_ptr(x), rows, k, x.stride(0),
                                       _global(global_scale, "global_scale", dev),
-                                      *_operand(out, "out", dev), _stream(stream))
+                                      *_output(out, rows, k, dev), _stream(stream))
     _check(st, "nvfp4_quantize_noalloc")
     return out
 
@@ -285,13 +310,23 @@ class Calibrator:
         return self.global_scale
 
 
-def _product(out: torch.Tensor, m: int, n: int, dev: int) -> tuple[int, int, int]:
-    """Checked [m, n] output of a product on cuda:``dev``: pointer, type, row pitch."""
-    if out.dtype not in (_BF16, _FP32) or out.shape != (m, n) or out.stride(1) != 1:
+_Y_TYPES = {_BF16: 0, _FP32: 1}
+
+
+def _product(out: torch.Tensor | None, dtype: torch.dtype, m: int, n: int, dev: int, like: torch.Tensor,
+             stream: torch.cuda.Stream | None):
+    """The [m, n] output of a product on cuda:``dev``, made or checked: (out,
+    (pointer, type, row pitch))."""
+    if out is None:
+        if dtype not in _Y_TYPES:
+            raise ValueError(f"out must be bf16/fp32, not {dtype}")
+        out = _given(_empty((m, n), dtype, like.device, stream), stream)
+        return out, (out.data_ptr(), _Y_TYPES[dtype], n)
+    if out.dtype not in _Y_TYPES or out.shape != (m, n) or out.stride(1) != 1:
         raise ValueError(f"out must be bf16/fp32 [{m}, {n}] with unit column stride")
     if out.get_device() != dev:
         raise ValueError(f"out must be on cuda:{dev}")
-    return out.data_ptr(), 0 if out.dtype is _BF16 else 1, out.stride(0)
+    return out, (out.data_ptr(), _Y_TYPES[out.dtype], out.stride(0))
 
 
 def _epilogue(bias: torch.Tensor | None, activation: str, residual: torch.Tensor | None,
@@ -333,11 +368,9 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out: torch.Tensor | None = None,
     if a.k != b.k:
         raise ValueError("k mismatch")
     m, n, k = a.rows, b.rows, a.k
-    if out is None:
-        out = _given(_empty((m, n), out_dtype, a.codes.device, stream), stream)
     dev = a.codes.get_device()
-    y = _product(out, m, n, dev)
     operands = (*_operand(a, "a", dev), *_operand(b, "b", dev))
+    out, y = _product(out, out_dtype, m, n, dev, a.codes, stream)
     ws, ws_bytes = _scratch(workspace, dev)
     if bias is not None or residual is not None or activation != "none":
         st = lib().nvfp4_gemm_epilogue(
@@ -373,16 +406,13 @@ def gemm_swiglu_quant(a: NVFP4Tensor, b_interleaved: NVFP4Tensor, h_global: torc
     m, ffn, k = a.rows, b_interleaved.rows // 2, a.k
     dev = a.codes.get_device()
     h_ptr = _global(h_global, "h_global", dev)
-    made = out is None
+    if out is None:
+        out = _empty_nvfp4(m, ffn, a.codes.device, stream)
     with _on(stream):
-        if made:
-            out = NVFP4Tensor.empty(m, ffn, a.codes.device)
         out.global_scale.copy_(h_global.reshape(1))
-    if made:
-        _given_nvfp4(out, stream)
     st = lib().nvfp4_gemm_swiglu_quant(*_operand(a, "a", dev),
                                        *_operand(b_interleaved, "b_interleaved", dev), h_ptr,
-                                       *_operand(out, "out", dev)[:2], m, ffn, k, _stream(stream))
+                                       *_output(out, m, ffn, dev)[:2], m, ffn, k, _stream(stream))
     _check(st, "nvfp4_gemm_swiglu_quant")
     return out
 
@@ -404,18 +434,15 @@ def gemm_swiglu_quant_dynamic(a: NVFP4Tensor, b_interleaved: NVFP4Tensor,
     if a.k != b_interleaved.k:
         raise ValueError("k mismatch")
     m, ffn, k = a.rows, b_interleaved.rows // 2, a.k
-    made = out is None
-    with _on(stream):
-        if made:
-            out = NVFP4Tensor.empty(m, ffn, a.codes.device)
-        if workspace is None:
+    if out is None:
+        out = _empty_nvfp4(m, ffn, a.codes.device, stream)
+    if workspace is None:
+        with _on(stream):
             workspace = swiglu_quant_dynamic_workspace(m, ffn, a.codes.device)
-    if made:
-        _given_nvfp4(out, stream)
     dev = a.codes.get_device()
     st = lib().nvfp4_gemm_swiglu_quant_dynamic(
         *_operand(a, "a", dev), *_operand(b_interleaved, "b_interleaved", dev),
-        *_operand(out, "out", dev), m, ffn, k, *_scratch(workspace, dev), _stream(stream))
+        *_output(out, m, ffn, dev), m, ffn, k, *_scratch(workspace, dev), _stream(stream))
     _check(st, "nvfp4_gemm_swiglu_quant_dynamic")
     return out
 
@@ -660,10 +687,8 @@ def linear(x: torch.Tensor, w: NVFP4Tensor, out: torch.Tensor | None = None,
     if k != w.k:
         raise ValueError("k mismatch")
     n = w.rows
-    if out is None:
-        out = _given(_empty((m, n), out_dtype, x.device, stream), stream)
     dev = x.get_device()
-    y = _product(out, m, n, dev)
+    out, y = _product(out, out_dtype, m, n, dev, x, stream)
     if workspace is None:
         with _on(stream):
             workspace = linear_workspace(m, n, k, x.device)

@@ -87,3 +87,55 @@ def test_a_bad_output_is_refused(world, what, bias):
             call(OUTPUTS[what]())
         call(fake(4, 64))
     assert len(launched(world[0])) == 2
+
+
+def spoilt(**parts):
+    t = nvfp4_tensor(64, 64)
+    return nv.NVFP4Tensor(**{**vars(t), **parts})
+
+
+OPERANDS = {
+    "codes too few": lambda: dict(codes=fake(63, 32, dtype=torch.uint8)),
+    "codes with gaps": lambda: dict(codes=fake(64, 64, dtype=torch.uint8)[:, ::2]),
+    "codes not 8 bits": lambda: dict(codes=fake(64, 32)),
+    "codes on the host": lambda: dict(codes=torch.ones(64, 32, dtype=torch.uint8)),
+    "scales too few": lambda: dict(sf=fake(511, dtype=torch.uint8)),
+    "scales with gaps": lambda: dict(sf=fake(8192, dtype=torch.uint8)[::2]),
+    "scales on the host": lambda: dict(sf=torch.ones(4096, dtype=torch.uint8)),
+    "more rows than it has": lambda: dict(rows=65),
+    "global on the host": lambda: dict(global_scale=torch.ones(1)),
+    "global not FP32": lambda: dict(global_scale=fake(1)),
+    "no global": lambda: dict(global_scale=fake(0, dtype=torch.float32)),
+}
+
+
+@pytest.mark.parametrize("what", OPERANDS)
+def test_a_bad_operand_is_refused(world, what):
+    h = fake(1, dtype=torch.float32)
+    for call in (lambda t: nv.gemm(nvfp4_tensor(4, 64), t), lambda t: nv.gemm(t, nvfp4_tensor(64, 64)),
+                 lambda t: nv.linear(fake(4, 64), t), lambda t: nv.linear(fake(4, 64), t, activation="silu"),
+                 lambda t: nv.quantize(fake(64, 64), out=t),
+                 lambda t: nv.gemm_swiglu_quant(t, nvfp4_tensor(256, 64), h),
+                 lambda t: nv.gemm_swiglu_quant_dynamic(t, nvfp4_tensor(256, 64))):
+        with pytest.raises(ValueError):
+            call(spoilt(**OPERANDS[what]()))
+    assert not launched(world[0])
+
+
+@pytest.mark.parametrize("rows,k", [(32, 64), (128, 64), (64, 32)])
+def test_an_nvfp4_output_of_another_size_is_refused(world, rows, k):
+    h, out = fake(1, dtype=torch.float32), nvfp4_tensor(rows, k)
+    for call in (lambda: nv.quantize(fake(64, 64), out=out), lambda: nv.quantize_noalloc(fake(64, 64), out),
+                 lambda: nv.gemm_swiglu_quant(nvfp4_tensor(64, 64), nvfp4_tensor(128, 64), h, out=out),
+                 lambda: nv.gemm_swiglu_quant_dynamic(nvfp4_tensor(64, 64), nvfp4_tensor(128, 64), out=out)):
+        with pytest.raises(ValueError):
+            call()
+    assert not launched(world[0])
+
+
+@pytest.mark.parametrize("call", [lambda: nv.linear(fake(4, 64), nvfp4_tensor(64, 64), out_dtype=torch.float16),
+                                  lambda: nv.gemm(nvfp4_tensor(4, 64), nvfp4_tensor(64, 64), out_dtype=torch.float64)])
+def test_a_bad_output_type_is_refused(world, call):
+    with pytest.raises(ValueError):
+        call()
+    assert not launched(world[0])

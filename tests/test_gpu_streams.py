@@ -91,3 +91,34 @@ def copy(t, stream):
     """A copy of `t` that belongs to `stream`."""
     with torch.cuda.stream(stream):
         return t.clone()
+
+
+def test_captured_on_a_forked_stream(nv, orc):
+    """Calls given a stream that a capture forked to, with buffers of their own:
+    the graph's replays give what the calls give."""
+    g = torch.Generator().manual_seed(9)
+    n, k = 640, 1024
+    x = torch.randn((37, k), generator=g).to(torch.bfloat16).cuda()
+    w = upload(orc.quantize(bits((torch.randn((n, k), generator=g) * 0.05).to(torch.bfloat16))))
+    bias = torch.randn(n, generator=g).to(torch.bfloat16).cuda()
+    q, kk, v = (torch.randn(90, 2, 64, generator=g).to(torch.bfloat16).cuda() * 0.1 for _ in range(3))
+    decay, beta = -torch.rand(90, 2, generator=g).cuda(), torch.rand(90, 2, generator=g).cuda()
+    s = torch.cuda.Stream()
+
+    def both(stream):
+        return (nv.linear(x, w, bias=bias, activation="gelu", stream=stream),
+                nv.linear_attention(q, kk, v, decay, beta, stream=stream))
+
+    both(None)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = both(s)
+        torch.cuda.current_stream().wait_stream(s)
+    for seed in (1, 2):
+        x.copy_(torch.randn((37, k), generator=g).to(torch.bfloat16))
+        v.copy_(torch.randn(90, 2, 64, generator=g).to(torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, both(None)))
+    assert nv.read_fault() == 0

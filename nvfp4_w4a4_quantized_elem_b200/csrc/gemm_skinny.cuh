@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(Cfg<BNT, FUSED>::THREADS, 1)
       const int n = wt * BW + nl;              // this thread's output column
       const bool n_ok = n < p.N;
       // EPI: this column's bias, and the residual of the tokens [m0, m0 + T)
-      // (bf16 bits; Y may be the residual, so every load of a group comes
+      // (as FP32; Y may be the residual, so every load of a group comes
       // before its stores); the first group's loads do not wait for the sum
       const float bias_n = EPI && p.epi.bias != nullptr && n_ok
                                ? __bfloat162float(p.epi.bias[n]) : 0.0f;

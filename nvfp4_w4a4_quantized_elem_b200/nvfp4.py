@@ -457,17 +457,25 @@ def fuse_group_scales(modules: list[NVFP4Tensor], sf_out: torch.Tensor | None = 
     k = modules[0].k
     total = sum(m.rows for m in modules)
     dev = modules[0].codes.device
+    index = modules[0].codes.get_device()
+    if any(m.k != k for m in modules):
+        raise ValueError("the modules of a group share k")
+    sf_in = [_operand(m, "every module", index)[1] for m in modules]
     if sf_out is None:
         sf_out = _given(_empty(sf_bytes(total, k), torch.uint8, dev, stream), stream)
+    elif (sf_out.get_device() != index or not sf_out.is_contiguous() or sf_out.element_size() != 1
+          or sf_out.numel() < sf_bytes(total, k)):
+        raise ValueError(f"sf_out must be {sf_bytes(total, k)} contiguous bytes on {dev}")
     if global_out is None:
         global_out = _given(_empty(1, torch.float32, dev, stream), stream)
+    global_ptr = _global(global_out, "global_out", index)
     with _on(stream):
         globals_in = torch.cat([m.global_scale for m in modules])
     rows = (ctypes.c_int64 * n)(*[m.rows for m in modules])
-    ptrs = (ctypes.c_void_p * n)(*[m.sf.data_ptr() for m in modules])
+    ptrs = (ctypes.c_void_p * n)(*sf_in)
     st = lib().nvfp4_fuse_group_scales(n, ctypes.cast(rows, ctypes.c_void_p), k,
                                        ctypes.cast(ptrs, ctypes.c_void_p), _ptr(globals_in),
-                                       _ptr(sf_out), _ptr(global_out), _stream(stream))
+                                       _ptr(sf_out), global_ptr, _stream(stream))
     _check(st, "nvfp4_fuse_group_scales")
     return sf_out, global_out
 
@@ -485,10 +493,14 @@ def silu_mul(y: torch.Tensor, out: torch.Tensor | None = None,
              stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """nvfp4_silu_mul: h = silu(y[:, :n]) * y[:, n:] in bf16."""
     _require_cuda(y, "y", torch.bfloat16)
-    m, n2 = y.shape
-    n = n2 // 2
+    if y.dim() != 2 or y.shape[1] % 2 or y.stride(1) != 1:
+        raise ValueError("y must be [m, 2n] with unit column stride")
+    m, n = y.shape[0], y.shape[1] // 2
     if out is None:
         out = _given(_empty((m, n), torch.bfloat16, y.device, stream), stream)
+    elif (out.shape != (m, n) or out.dtype is not _BF16 or out.device != y.device
+          or out.stride(1) != 1):
+        raise ValueError(f"out must be bf16 [{m}, {n}] with unit column stride on {y.device}")
     st = lib().nvfp4_silu_mul(_ptr(y), m, n, y.stride(0), _ptr(out), out.stride(0),
                               _stream(stream))
     _check(st, "nvfp4_silu_mul")

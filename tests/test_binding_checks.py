@@ -139,3 +139,30 @@ def test_a_bad_output_type_is_refused(world, call):
     with pytest.raises(ValueError):
         call()
     assert not launched(world[0])
+
+
+def test_a_group_of_modules_is_checked(world):
+    a, b = nvfp4_tensor(4, 64), nvfp4_tensor(8, 64)
+    nv.fuse_group_scales([a, b])
+    nv.fuse_group_scales([a, b], sf_out=fake(4096, dtype=torch.uint8), global_out=fake(1, dtype=torch.float32))
+    assert len(launched(world[0])) == 2
+    for modules, kw in (([a, nvfp4_tensor(8, 128)], {}),
+                        ([a, spoilt(sf=torch.ones(4096, dtype=torch.uint8))], {}),
+                        ([a, b], dict(sf_out=fake(4095, dtype=torch.uint8))),
+                        ([a, b], dict(sf_out=torch.ones(4096, dtype=torch.uint8))),
+                        ([a, b], dict(sf_out=fake(8192, dtype=torch.uint8)[::2])),
+                        ([a, b], dict(global_out=torch.ones(1))), ([a, b], dict(global_out=fake(1)))):
+        with pytest.raises(ValueError):
+            nv.fuse_group_scales(modules, **kw)
+    assert len(launched(world[0])) == 2
+
+
+def test_silu_mul_is_checked(world):
+    nv.silu_mul(fake(4, 64), out=fake(4, 32))
+    assert len(launched(world[0])) == 1
+    for y, out in ((fake(4, 63), None), (fake(64, 4).t(), None), (fake(256), None), (fake(4, 64), fake(3, 32)),
+                   (fake(4, 64), fake(4, 64)), (fake(4, 64), fake(4, 32, dtype=torch.float32)),
+                   (fake(4, 64), fake(32, 4).t()), (fake(4, 64), torch.ones(4, 32, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            nv.silu_mul(y, out=out)
+    assert len(launched(world[0])) == 1
